@@ -1,6 +1,8 @@
 // Internal helpers shared by the libmoe CUDA sources.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -32,6 +34,23 @@ __device__ __forceinline__ void flag(int32_t *status, int bit) {
 
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// The two 16-bit element types and fp32 behind one name.
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+
+inline bool half_type(int dtype) { return dtype == MOE_BF16 || dtype == MOE_FP16; }
+inline bool out_type_ok(int dtype, int out_dtype) { return out_dtype == dtype || out_dtype == MOE_FP32; }
+inline bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 inline bool dims_ok(int d, int f) {
     return d > 0 && f > 0 && d % 256 == 0 && f % 256 == 0 && d <= kMaxDim && f <= kMaxDim;

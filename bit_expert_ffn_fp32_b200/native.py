@@ -19,6 +19,8 @@ LIB_PATH = os.path.join(PKG, "libmoe.so")
 MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
                 4: "MOE_ERR_CUDA", 5: "MOE_ERR_OVERFLOW", 6: "MOE_ERR_HOST"}
+BF16, FP16, FP32 = 0, 1, 2
+ACT_NONE, ACT_SWIGLU = 0, 1
 DEV_BAD_INDEX, DEV_BAD_SLOT, DEV_NONFINITE, DEV_MISS_OVERFLOW, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
 
 _P = C.c_void_p
@@ -34,6 +36,11 @@ class QPool(C.Structure):
 
 class QMatrix(C.Structure):
     _fields_ = [("codes", _P), ("hi", _P), ("scale", _P), ("min", _P)]
+
+
+class Q4Weights(C.Structure):
+    _fields_ = [("codes", _P), ("scale", _P), ("min", _P), ("num_slots", _I32), ("N", _I32), ("K", _I32),
+                ("group", _I32)]
 
 
 class Swap(C.Structure):
@@ -74,6 +81,13 @@ SIGNATURES = {
                               _P, _I32, _P, _P, _P, _SZ, _P, _P]),
     "moe_complete_misses_host": (_I, [_I, _I, _I, _P, _I, _P, _I32, _I32, _P, _I, _P, _I]),
     "moe_debug_wait_probe": (_I, [_P, C.c_uint32, _P, _P, _P]),
+    "moe_linear_q4": (_I, [_P, _I32, _P, _I, _I, _I, _P, _I, _P]),
+    "moe_expert_linear_q4": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _I, _P, _P]),
+    "moe_expert_gemm": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P]),
+    "moe_expert_gemm_dgrad": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P, _P]),
+    "moe_expert_gemm_wgrad": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P]),
+    "moe_swiglu": (_I, [_P, _I, C.c_int64, _I, _P, _P]),
+    "moe_swiglu_backward": (_I, [_P, _P, _I, C.c_int64, _I, _P, _P]),
     "moe_miss_engine_create": (_I, [_I, C.POINTER(_P)]),
     "moe_miss_engine_submit": (_I, [_P, _I, _I, _I, _P, _I, _P, _P, _I32, _I32, _P, _I, _P]),
     "moe_miss_engine_wait": (_I, [_P]),
@@ -336,3 +350,154 @@ def debug_wait_probe(counter, target: int, elapsed_ns, dev_status, stream=None) 
     target and an mbarrier phase nothing completes (device tensors)."""
     check("moe_debug_wait_probe", lib.moe_debug_wait_probe(ptr(counter), target, ptr(elapsed_ns), ptr(dev_status),
                                                            stream_handle(stream)))
+
+
+# ------------------------------------------------------------------ 4-bit and unquantised products, gradients
+def _codes_of_dtypes() -> dict:
+    import torch
+    # int16 tensors hold bf16 bits, as for the layer's x
+    return {torch.bfloat16: BF16, torch.int16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+
+_DTYPES: dict = {}
+
+
+def dtype_code(t) -> int:
+    """moe_dtype of a tensor (int16 = bf16 bits)."""
+    if not _DTYPES:
+        _DTYPES.update(_codes_of_dtypes())
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"no moe_dtype for {t.dtype}: bfloat16 (or int16 bits), float16 and float32 are known")
+    return code
+
+
+def _same_place(*sized) -> int:
+    """Check (tensor, elements) pairs before their addresses go to the library:
+    contiguous tensors of one GPU, the current one, of at least so many
+    elements. Returns the GPU's index."""
+    dev = sized[0][0].get_device()
+    for t, n in sized:
+        if t is not None and not (t.numel() >= n and t.is_contiguous() and t.get_device() == dev):
+            raise ValueError(f"a contiguous tensor of {n} or more elements on GPU {dev} is wanted, got "
+                             f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    import torch
+    if dev < 0:
+        raise ValueError("GPU tensors are wanted")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on GPU {dev}, the current GPU is {torch.cuda.current_device()}")
+    return dev
+
+
+def _int32(*tensors) -> None:
+    import torch
+    for t in tensors:
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"an int32 tensor is wanted, got {t.dtype}")
+
+
+def q4_weights(codes, scale, min, group: int) -> Q4Weights:
+    """moe_q4weights over codes uint8 [slots][N][K/2], scale and min fp16
+    [slots][N][K/group] (min None: w = s*(q-8)); one matrix may leave the slots
+    out. The description keeps the tensors alive."""
+    import torch
+    if codes.dtype != torch.uint8 or codes.dim() not in (2, 3):
+        raise ValueError("codes: uint8 [slots][N][K/2]")
+    slots, N, half = codes.shape if codes.dim() == 3 else (1, *codes.shape)
+    if group not in (32, 64, 128) or 2 * half % group:
+        raise ValueError("group: 32, 64 or 128, a divisor of K")
+    for t in (scale, min):
+        if t is not None and (t.dtype not in (torch.float16, torch.int16) or
+                              t.shape != (*codes.shape[:-1], 2 * half // group)):
+            raise ValueError("scale, min: fp16 [slots][N][K/group]")
+    for t in (codes, scale, min):
+        if t is not None and not (t.is_contiguous() and t.device == codes.device):
+            raise ValueError("codes, scale, min: contiguous, on one GPU")
+    w = Q4Weights(ptr(codes), ptr(scale), ptr(min), slots, N, 2 * half, group)
+    w.tensors = (codes, scale, min)
+    return w
+
+
+def linear_q4(W: Q4Weights, slot: int, x, T: int, out, act: int = ACT_NONE, stream=None) -> None:
+    """out[t] = W[slot] x[t]; out [T][N] (SwiGLU: [T][N/2]) in x's type or fp32."""
+    _same_place((W.tensors[0], 0), (x, T * W.K), (out, T * W.N // (1 + act)))
+    check("moe_linear_q4", lib.moe_linear_q4(C.addressof(W), slot, ptr(x), dtype_code(x), T, act, ptr(out),
+                                             dtype_code(out), stream_handle(stream)))
+
+
+def expert_linear_q4(W: Q4Weights, slot_of, x, T: int, E: int, k: int, offsets, sorted_tok, active, out,
+                     act: int = ACT_NONE, dev_status=None, stream=None) -> None:
+    """out[s] = W[slot_of[e]] x_s for the sorted pairs s of every active expert e
+    (x_s = x[sorted_tok[s]], or x[s] with sorted_tok None)."""
+    P = T * k
+    _same_place((W.tensors[0], 0), (slot_of, E), (x, (P if sorted_tok is None else T) * W.K), (offsets, E + 1),
+                (sorted_tok, P), (active, E + 1), (out, P * W.N // (1 + act)), (dev_status, 1))
+    _int32(slot_of, offsets, sorted_tok, active, dev_status)
+    check("moe_expert_linear_q4",
+          lib.moe_expert_linear_q4(C.addressof(W), ptr(slot_of), ptr(x), dtype_code(x), T, E, k, ptr(offsets),
+                                   ptr(sorted_tok), ptr(active), act, ptr(out), dtype_code(out), ptr(dev_status),
+                                   stream_handle(stream)))
+
+
+def expert_gemm(a, W, T: int, E: int, k: int, N: int, K: int, offsets, sorted_tok, out, dev_status=None,
+                stream=None) -> None:
+    """out[s] = W[e] a_s for the sorted pairs s of every expert e
+    (a_s = a[sorted_tok[s]], or a[s] with sorted_tok None)."""
+    P = T * k
+    _same_place((a, (P if sorted_tok is None else T) * K), (W, E * N * K), (offsets, E + 1), (sorted_tok, P),
+                (out, P * N), (dev_status, 1))
+    _int32(offsets, sorted_tok, dev_status)
+    dt = dtype_code(a)
+    if dtype_code(W) != dt:
+        raise ValueError("a and W have one type")
+    check("moe_expert_gemm", lib.moe_expert_gemm(ptr(a), ptr(W), dt, T, E, k, N, K, ptr(offsets), ptr(sorted_tok),
+                                                 ptr(out), dtype_code(out), ptr(dev_status), stream_handle(stream)))
+
+
+def expert_gemm_dgrad(dy, W, T: int, E: int, k: int, N: int, K: int, offsets, da, dev_status=None,
+                      stream=None) -> None:
+    """da[s] = W[e]^T dy[s] for the sorted pairs s of every expert e."""
+    P = T * k
+    _same_place((dy, P * N), (W, E * N * K), (offsets, E + 1), (da, P * K), (dev_status, 1))
+    _int32(offsets, dev_status)
+    dt = dtype_code(dy)
+    if dtype_code(W) != dt:
+        raise ValueError("dy and W have one type")
+    check("moe_expert_gemm_dgrad",
+          lib.moe_expert_gemm_dgrad(ptr(dy), ptr(W), dt, T, E, k, N, K, ptr(offsets), ptr(da), dtype_code(da),
+                                    ptr(dev_status), stream_handle(stream)))
+
+
+def expert_gemm_wgrad(dy, a, T: int, E: int, k: int, N: int, K: int, offsets, sorted_tok, dW, base=None,
+                      dev_status=None, stream=None) -> None:
+    """dW[e] = base[e] + sum over expert e's sorted pairs s of dy[s] a_s^T (base
+    None: zeros; base may be dW)."""
+    P = T * k
+    _same_place((dy, P * N), (a, (P if sorted_tok is None else T) * K), (offsets, E + 1), (sorted_tok, P),
+                (dW, E * N * K), (base, E * N * K), (dev_status, 1))
+    _int32(offsets, sorted_tok, dev_status)
+    dt, odt = dtype_code(dy), dtype_code(dW)
+    if dtype_code(a) != dt or (base is not None and dtype_code(base) != odt):
+        raise ValueError("dy and a have one type, base and dW have one type")
+    check("moe_expert_gemm_wgrad",
+          lib.moe_expert_gemm_wgrad(ptr(dy), ptr(a), dt, T, E, k, N, K, ptr(offsets), ptr(sorted_tok), ptr(base),
+                                    ptr(dW), odt, ptr(dev_status), stream_handle(stream)))
+
+
+def swiglu(gu, rows: int, f: int, h, stream=None) -> None:
+    """h = silu(g) * u for rows [g | u] of gu."""
+    _same_place((gu, rows * 2 * f), (h, rows * f))
+    dt = dtype_code(gu)
+    if dtype_code(h) != dt:
+        raise ValueError("gu and h have one type")
+    check("moe_swiglu", lib.moe_swiglu(ptr(gu), dt, rows, f, ptr(h), stream_handle(stream)))
+
+
+def swiglu_backward(gu, dh, rows: int, f: int, dgu, stream=None) -> None:
+    """dgu = the gradient of swiglu to [g | u], given dh."""
+    _same_place((gu, rows * 2 * f), (dh, rows * f), (dgu, rows * 2 * f))
+    dt = dtype_code(gu)
+    if dtype_code(dh) != dt or dtype_code(dgu) != dt:
+        raise ValueError("gu, dh and dgu have one type")
+    check("moe_swiglu_backward", lib.moe_swiglu_backward(ptr(gu), ptr(dh), dt, rows, f, ptr(dgu),
+                                                         stream_handle(stream)))

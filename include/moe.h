@@ -482,6 +482,119 @@ moe_status moe_expert_ffn_q2_noalloc(const moe_qpool *W, const int32_t *slot_of,
 moe_status moe_combine(const float *y_perm, const int32_t *inv, const float *topk_w, const int32_t *slot_of_pair,
                        const float *y_shared, int T, int k, int d, float *y, moe_stream_t stream);
 
+/* ------------------------------------------------------------------ */
+/* Products with 4-bit weights                                         */
+/* ------------------------------------------------------------------ */
+
+/* Element types of the calls below. */
+typedef enum moe_dtype { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
+
+/* What a 4-bit product does with its rows before they are written. */
+typedef enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SWIGLU = 1 /* out[i] = silu(y[i]) * y[i + N/2], i < N/2 */
+} moe_act;
+
+/*
+ * num_slots matrices [N][K] of 4-bit weights with one scale (and, if min is not
+ * NULL, one offset) per group of `group` weights along K, read as they are (no
+ * packed record):
+ *   codes  uint8 [num_slots][N][K/2]: weight k's code at byte k/2, the low
+ *          half for even k; 16-byte aligned
+ *   scale  fp16 bits [num_slots][N][K/group]; 2-byte aligned
+ *   min    fp16 bits, same shape, or NULL
+ * Weight: w = s*q + m with min, w = s*(q-8) without, q in 0..15.
+ * group is 32, 64 or 128; K a multiple of group, N a multiple of 32, both up
+ * to 16384.
+ */
+typedef struct moe_q4weights {
+    const uint8_t *codes;
+    const uint16_t *scale;
+    const uint16_t *min; /* NULL: w = s*(q-8) */
+    int32_t num_slots;
+    int32_t N;
+    int32_t K;
+    int32_t group;
+} moe_q4weights;
+
+/*
+ * out[t] = W[slot] x[t] for T rows x (a projection next to the layer).
+ *   x    bf16 or fp16 [T][K] (dtype), 16-byte aligned
+ *   out  [T][N], with MOE_ACT_SWIGLU [T][N/2], in out_dtype: x's type or MOE_FP32
+ * Codes enter the products exactly; sums run in fp32 and are scaled group by
+ * group in fp32, so no weight is rounded. The order of the additions depends
+ * on the sizes only: equal calls give equal bits.
+ */
+moe_status moe_linear_q4(const moe_q4weights *W, int32_t slot, const void *x, int dtype, int T, int act, void *out,
+                         int out_dtype, moe_stream_t stream);
+
+/*
+ * The same for the T*k sorted pairs of moe_permute: out[s] = W[slot_of[e]] x_s
+ * for every expert e of `active` and its rows s = offsets[e] .. offsets[e+1].
+ *   slot_of     int32 [E]: slot of each expert, -1 = skip (its rows of out are
+ *               left as they were); other values outside the slots set
+ *               MOE_DEV_BAD_SLOT and are skipped as well
+ *   x           sorted_tok given: [T][K], x_s = x[sorted_tok[s]] (a token
+ *               outside [0,T) sets MOE_DEV_BAD_INDEX and counts as zeros);
+ *               sorted_tok NULL: [T*k][K], x_s = x[s]
+ *   offsets, active  int32 [E+1] each, from moe_permute; an expert id or a row
+ *               range outside its bounds sets MOE_DEV_BAD_INDEX and is skipped
+ *   out         [T*k][N] or, with MOE_ACT_SWIGLU, [T*k][N/2]
+ */
+moe_status moe_expert_linear_q4(const moe_q4weights *W, const int32_t *slot_of, const void *x, int dtype, int T, int E,
+                                int k, const int32_t *offsets, const int32_t *sorted_tok, const int32_t *active,
+                                int act, void *out, int out_dtype, int32_t *dev_status, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Unquantised expert products and their gradients                     */
+/* ------------------------------------------------------------------ */
+
+/*
+ * Matrix products grouped by expert over the sorted pairs of moe_permute, for
+ * experts kept in 16 bits: expert e owns rows s = offsets[e] .. offsets[e+1].
+ *   moe_expert_gemm        out[s] = W[e] a_s
+ *   moe_expert_gemm_dgrad  da[s]  = W[e]^T dy[s]
+ *   moe_expert_gemm_wgrad  dW[e]  = base[e] + sum over its rows of dy[s] a_s^T
+ *   W, dW, base  [E][N][K]
+ *   a            sorted_tok given: [T][K], a_s = a[sorted_tok[s]] (a token
+ *                outside [0,T) sets MOE_DEV_BAD_INDEX and counts as zeros);
+ *                sorted_tok NULL: [T*k][K], a_s = a[s]
+ *   dy, out      [T*k][N];  da [T*k][K]
+ *   base         NULL (zeros), or the sum so far; may be dW itself
+ *   dtype        of the inputs: MOE_BF16 or MOE_FP16; out_dtype, of out, da or
+ *                dW and base: the same or MOE_FP32
+ *   offsets      int32 [E+1], within [0, T*k] and not decreasing; an expert
+ *                whose range is not sets MOE_DEV_BAD_INDEX and has no rows
+ * Rows that belong to no expert are left as they were; dW is written for every
+ * expert, also those without rows. Sums run in fp32, rounded once; their order
+ * depends on the sizes only. N and K are multiples of 8 up to 16384, E <= 4096;
+ * all tensors but offsets and sorted_tok 16-byte aligned; outputs overlap no
+ * input (but base).
+ */
+moe_status moe_expert_gemm(const void *a, const void *W, int dtype, int T, int E, int k, int N, int K,
+                           const int32_t *offsets, const int32_t *sorted_tok, void *out, int out_dtype,
+                           int32_t *dev_status, moe_stream_t stream);
+moe_status moe_expert_gemm_dgrad(const void *dy, const void *W, int dtype, int T, int E, int k, int N, int K,
+                                 const int32_t *offsets, void *da, int out_dtype, int32_t *dev_status,
+                                 moe_stream_t stream);
+moe_status moe_expert_gemm_wgrad(const void *dy, const void *a, int dtype, int T, int E, int k, int N, int K,
+                                 const int32_t *offsets, const int32_t *sorted_tok, const void *base, void *dW,
+                                 int out_dtype, int32_t *dev_status, moe_stream_t stream);
+
+/*
+ * The activation between the gate/up and the down product, for rows
+ * [g | u] of gu (dtype MOE_BF16 or MOE_FP16, [rows][2f], as moe_expert_gemm
+ * writes them for weights with the gate rows first), and its gradient:
+ *   moe_swiglu           h = silu(g) * u                              [rows][f]
+ *   moe_swiglu_backward  dg = dh * u * sig(g) * (1 + g * (1 - sig(g))),
+ *                        du = dh * silu(g)                     dgu [rows][2f]
+ * in fp32, rounded once. f is a multiple of 8; all tensors 16-byte aligned.
+ * dgu may be gu itself; otherwise outputs overlap no input.
+ */
+moe_status moe_swiglu(const void *gu, int dtype, int64_t rows, int f, void *h, moe_stream_t stream);
+moe_status moe_swiglu_backward(const void *gu, const void *dh, int dtype, int64_t rows, int f, void *dgu,
+                               moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
