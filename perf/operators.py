@@ -217,9 +217,11 @@ def _own(s):
     elif c["op"] == "dgrad":
         native.expert_gemm_dgrad(s["dy"], s["W"], T, E, k, N, K, s["offsets"], out)
     else:
+        base = s["before"] if c["accumulate"] else None
+        if base is not None and base.dtype == torch.float32:
+            out = base  # an fp32 sum is added to in place
         native.expert_gemm_wgrad(s["dy"], s["a"], T, E, k, N, K, s["offsets"],
-                                 s["sorted_tok"] if c["gather"] else None, out,
-                                 base=s["before"] if c["accumulate"] else None)
+                                 s["sorted_tok"] if c["gather"] else None, out, base=base)
     return out
 
 
