@@ -2,6 +2,13 @@
 // expert, and its gradient:
 //   h = silu(g) * u,  dg = dh * u * sig(g) * (1 + g * (1 - sig(g))),  du = dh * silu(g)
 // elementwise in fp32 from 16-bit tensors, rounded once.
+//
+// Bound by memory: 6 bytes an element forward, 10 backward. A thread takes two
+// chunks of 8 elements (16-byte loads of every operand, all issued before the
+// first is used), a block 512 chunks in a row; blocks are not persistent, so
+// the loads of one cover the stores of another. sig(g) is formed with the
+// hardware's exp2 and reciprocal (a few units of 2^-22, against half a step of
+// 2^-11 or 2^-8 in the result).
 #include <algorithm>
 
 #include "common.cuh"
@@ -9,24 +16,101 @@
 namespace moe {
 namespace {
 
+constexpr int kThreads = 256, kChunks = 2, kTile = kThreads * kChunks;
+
 template <typename E>
-__global__ void swiglu_kernel(const E *__restrict__ gu, int64_t n, int f, E *__restrict__ h) {
-    for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
-        const int64_t r = i / f, c = i - r * f;
-        const float g = to_f32(gu[r * 2 * f + c]), u = to_f32(gu[r * 2 * f + f + c]);
-        h[i] = from_f32<E>(g / (1.0f + expf(-g)) * u);
+struct Pack2;
+template <>
+struct Pack2<__nv_bfloat16> {
+    static __device__ float2 load(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
+    static __device__ uint32_t store(float a, float b) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+};
+template <>
+struct Pack2<__half> {
+    static __device__ float2 load(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+    static __device__ uint32_t store(float a, float b) {
+        const __half2 r = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+};
+
+// 1 / (1 + exp(-g)); 0 where exp(-g) passes 2^126, 1 for large g.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+// Chunk i of this block's tile: its row, and its first element in the row.
+// chunks_of_row = f / 8; div = ceil(2^32 / chunks_of_row) divides the small
+// numbers that are left inside a tile exactly.
+struct Where {
+    int64_t row;
+    int col;
+    bool in;
+};
+__device__ __forceinline__ Where where(int64_t row0, uint32_t chunk0, uint32_t i, uint32_t chunks_of_row, uint32_t div,
+                                       int64_t left) {
+    const uint32_t c = chunk0 + i;
+    const uint32_t q = chunks_of_row == 1 ? c : __umulhi(c, div);
+    return {row0 + q, int(c - q * chunks_of_row) * 8, int64_t(i) < left};
+}
+
+template <typename E, bool BACKWARD>
+__global__ void __launch_bounds__(kThreads) swiglu_kernel(const E *gu, const E *__restrict__ dh, int64_t chunks, int f,
+                                                          uint32_t div, E *out) {
+    const uint32_t cr = uint32_t(f) / 8;
+    const int64_t first = int64_t(blockIdx.x) * kTile, row0 = first / cr;
+    const uint32_t chunk0 = uint32_t(first - row0 * cr);
+    uint4 g[kChunks], u[kChunks], d[kChunks];
+    Where w[kChunks];
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+        w[j] = where(row0, chunk0, j * kThreads + threadIdx.x, cr, div, chunks - first);
+        if (w[j].in) {
+            const E *r = gu + w[j].row * 2 * f + w[j].col;
+            g[j] = *reinterpret_cast<const uint4 *>(r);
+            u[j] = *reinterpret_cast<const uint4 *>(r + f);
+            if (BACKWARD) d[j] = __ldg(reinterpret_cast<const uint4 *>(dh + w[j].row * f + w[j].col));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+        if (!w[j].in) continue;
+        const uint32_t gv[4] = {g[j].x, g[j].y, g[j].z, g[j].w}, uv[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+        uint32_t a[4], b[4];
+        if (!BACKWARD) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 gf = Pack2<E>::load(gv[i]), uf = Pack2<E>::load(uv[i]);
+                a[i] = Pack2<E>::store(gf.x * sigmoid(gf.x) * uf.x, gf.y * sigmoid(gf.y) * uf.y);
+            }
+            *reinterpret_cast<uint4 *>(out + w[j].row * f + w[j].col) = make_uint4(a[0], a[1], a[2], a[3]);
+        } else {
+            const uint32_t dv[4] = {d[j].x, d[j].y, d[j].z, d[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 gf = Pack2<E>::load(gv[i]), uf = Pack2<E>::load(uv[i]), df = Pack2<E>::load(dv[i]);
+                const float sx = sigmoid(gf.x), sy = sigmoid(gf.y);
+                a[i] = Pack2<E>::store(df.x * uf.x * sx * (1.0f + gf.x * (1.0f - sx)),
+                                       df.y * uf.y * sy * (1.0f + gf.y * (1.0f - sy)));
+                b[i] = Pack2<E>::store(df.x * gf.x * sx, df.y * gf.y * sy);
+            }
+            E *r = out + w[j].row * 2 * f + w[j].col;
+            *reinterpret_cast<uint4 *>(r) = make_uint4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<uint4 *>(r + f) = make_uint4(b[0], b[1], b[2], b[3]);
+        }
     }
 }
 
-template <typename E>
-__global__ void swiglu_backward_kernel(const E *gu, const E *__restrict__ dh, int64_t n, int f, E *dgu) {
-    for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
-        const int64_t r = i / f, c = i - r * f;
-        const float g = to_f32(gu[r * 2 * f + c]), u = to_f32(gu[r * 2 * f + f + c]), d = to_f32(dh[i]);
-        const float sig = 1.0f / (1.0f + expf(-g));
-        dgu[r * 2 * f + c] = from_f32<E>(d * u * sig * (1.0f + g * (1.0f - sig)));
-        dgu[r * 2 * f + f + c] = from_f32<E>(d * g * sig);
-    }
+template <typename E, bool BACKWARD>
+moe_status launch(const void *gu, const void *dh, int64_t rows, int f, void *out, cudaStream_t stream) {
+    const int64_t chunks = rows * (f / 8), blocks = (chunks + kTile - 1) / kTile;
+    if (blocks >= (int64_t(1) << 31)) return MOE_ERR_OVERFLOW;
+    const uint64_t cr = uint64_t(f) / 8;
+    swiglu_kernel<E, BACKWARD><<<unsigned(blocks), kThreads, 0, stream>>>(
+        static_cast<const E *>(gu), static_cast<const E *>(dh), chunks, f,
+        uint32_t(((uint64_t(1) << 32) + cr - 1) / cr), static_cast<E *>(out));
+    return launch_status();
 }
 
 moe_status check_swiglu(int dtype, int64_t rows, int f) {
@@ -45,15 +129,8 @@ MOE_API moe_status moe_swiglu(const void *gu, int dtype, int64_t rows, int f, vo
     const moe_status st = check_swiglu(dtype, rows, f);
     if (st != MOE_OK || rows == 0) return st;
     if (!gu || !h || !aligned16(gu) || !aligned16(h)) return MOE_ERR_INVALID_ARG;
-    const int64_t n = rows * f;
-    const int grid = int(std::min<int64_t>((n + 255) / 256, 148 * 16));
-    if (dtype == MOE_BF16)
-        swiglu_kernel<<<grid, 256, 0, as_cuda(stream)>>>(static_cast<const __nv_bfloat16 *>(gu), n, f,
-                                                         static_cast<__nv_bfloat16 *>(h));
-    else
-        swiglu_kernel<<<grid, 256, 0, as_cuda(stream)>>>(static_cast<const __half *>(gu), n, f,
-                                                         static_cast<__half *>(h));
-    return launch_status();
+    return dtype == MOE_BF16 ? launch<__nv_bfloat16, false>(gu, nullptr, rows, f, h, as_cuda(stream))
+                             : launch<__half, false>(gu, nullptr, rows, f, h, as_cuda(stream));
 }
 
 MOE_API moe_status moe_swiglu_backward(const void *gu, const void *dh, int dtype, int64_t rows, int f, void *dgu,
@@ -61,15 +138,6 @@ MOE_API moe_status moe_swiglu_backward(const void *gu, const void *dh, int dtype
     const moe_status st = check_swiglu(dtype, rows, f);
     if (st != MOE_OK || rows == 0) return st;
     if (!gu || !dh || !dgu || !aligned16(gu) || !aligned16(dh) || !aligned16(dgu)) return MOE_ERR_INVALID_ARG;
-    const int64_t n = rows * f;
-    const int grid = int(std::min<int64_t>((n + 255) / 256, 148 * 16));
-    if (dtype == MOE_BF16)
-        swiglu_backward_kernel<<<grid, 256, 0, as_cuda(stream)>>>(
-            static_cast<const __nv_bfloat16 *>(gu), static_cast<const __nv_bfloat16 *>(dh), n, f,
-            static_cast<__nv_bfloat16 *>(dgu));
-    else
-        swiglu_backward_kernel<<<grid, 256, 0, as_cuda(stream)>>>(static_cast<const __half *>(gu),
-                                                                  static_cast<const __half *>(dh), n, f,
-                                                                  static_cast<__half *>(dgu));
-    return launch_status();
+    return dtype == MOE_BF16 ? launch<__nv_bfloat16, true>(gu, dh, rows, f, dgu, as_cuda(stream))
+                             : launch<__half, true>(gu, dh, rows, f, dgu, as_cuda(stream));
 }
