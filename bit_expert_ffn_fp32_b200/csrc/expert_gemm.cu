@@ -12,13 +12,16 @@
 //   forward  n     pairs   k            W[e][n][k], K-major    a rows, K-major
 //   dgrad    k     pairs   n            W[e][n][k], MN-major   dy rows, K-major
 //   wgrad    k     n       pairs        a rows, MN-major       dy rows, MN-major
-// The operands come by TMA in the 128-byte swizzle, rows picked by token with
-// gathering loads (four rows each). Rows past an expert's end fall into columns
-// that are never written; in wgrad, where they would be summed, the last stage
-// is loaded row by row with an index past the tensor for them, which reads
-// zeros. Warps: loads, MMA issue, eight for the epilogue; two accumulators, so
-// that the epilogue of one tile runs beside the products of the next. Every
-// wait is bounded and sets MOE_DEV_TIMEOUT.
+// Wide tiles are computed by pairs of CTAs (cta_group::2, M = 256): each loads
+// its own half of A and of B, which cuts the L2 traffic of a 160-row tile by a
+// quarter and is what bounds experts of that size. Operands come by TMA in the
+// 128-byte swizzle, except rows picked by token and wgrad's last stage of an
+// expert (rows past its end must read as zeros there, as they are summed):
+// those are written by four warps with 16-byte cp.async in the same swizzle
+// (gathering TMA loads of four rows took about 48 cycles each, ten bytes a
+// cycle). Warps: TMA, MMA issue, eight for the epilogue, four that gather; two
+// accumulators, so that the epilogue of one tile runs beside the products of
+// the next. Every wait is bounded and sets MOE_DEV_TIMEOUT.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -33,15 +36,17 @@ namespace {
 
 enum Pass { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kTileM = 128;      // rows of tensor memory
+constexpr int kTileM = 128;      // rows of tensor memory of a CTA
 constexpr int kTileI = 64;       // contracted index a stage: 128 bytes, one swizzle row
-constexpr int kLoadWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kLoadWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 8, kPickWarp0 = kEpiWarp0 + kEpiWarps;
+constexpr int kPickWarps = 4;    // each gathers every fourth stage
 constexpr int kMaxStages = 10;
+constexpr int kTurn = 2048;      // per epilogue warp: 32 x 32 16-bit values on their way to 16-byte stores
 constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
 
 struct GemmParams {
     const int32_t *offsets, *sorted_tok;  // sorted_tok: rows of the gathered operand, or NULL
+    const uint16_t *rows, *dy;            // a (forward, wgrad), as the gathering warps read it; wgrad's dy
     const void *base;
     void *out;
     int rows_a;      // rows of the operand that sorted_tok picks from (T), or P
@@ -53,27 +58,33 @@ struct GemmParams {
 };
 
 // Tensor maps. w: weights [E][N][K]; rows, rows16: 64- and 16-row boxes of the
-// 16-bit rows that are N (forward, dgrad) or M (wgrad); pick: single rows of
-// the same; dy, dy_pick: wgrad's other operand.
+// rows that are N (forward, dgrad) or M (wgrad); dy: wgrad's other operand.
 struct GemmMaps {
-    CUtensorMap w, rows, rows16, pick, dy, dy_pick;
+    CUtensorMap w, rows, rows16, dy;
 };
 
 struct GemmSmem {
     uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
     uint32_t tmem_base;
     int abort;
-    int warp_sum[kThreads / 32];
+    int warp_sum[kPickWarp0 + kPickWarps];
     int prefix[kMaxE + 1];  // tiles before expert e
 };
 
-template <int PASS, int TN>
+// CG: CTAs that share a tile; TN: columns of a tile; PICK: with gathering warps.
+template <int PASS_, int CG_, int TN_, bool PICK_>
 struct Cfg {
-    static constexpr int kA = kTileM * 128, kB = TN * 128, kStage = kA + kB;
+    static constexpr int PASS = PASS_, CG = CG_, TN = TN_;
+    static constexpr bool PICK = PICK_;
+    static constexpr int kThreads = 32 * (PICK ? kPickWarp0 + kPickWarps : kPickWarp0);
+    static constexpr int kBRows = TN / CG;  // of B a CTA holds
+    static constexpr int kA = kTileM * 128, kB = kBRows * 128, kStage = kA + kB;
     // what fits beside the tables in 227 KB
-    static constexpr int kFit = (232448 - int(sizeof(GemmSmem)) - 1024) / kStage;
+    static constexpr int kFit = (232448 - int(sizeof(GemmSmem)) - 1024 - kEpiWarps * kTurn) / kStage;
     static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-    static constexpr int kSmem = kStages * kStage + 1024;
+    static constexpr int kSmem = kStages * kStage + kEpiWarps * kTurn + 1024;
+    static constexpr int kCols = 2 * TN;    // tensor memory: two accumulators
+    static_assert(kStages >= 4 && kCols >= 32 && kCols <= 512, "tile does not fit");
 };
 
 __device__ __forceinline__ void stop(GemmSmem &s, int32_t *status) {
@@ -88,25 +99,19 @@ __device__ __forceinline__ bool range_of(const GemmParams &p, int e, int &r0, in
     return false;
 }
 
-template <int PASS, int TN>
-__device__ __forceinline__ int tiles_of(const GemmParams &p, int e, int r0, int r1, int MT) {
-    if (PASS != kWgrad) return MT * ((r1 - r0 + TN - 1) / TN);
-    // an expert without rows: nothing to do where the sum so far is in place
-    return r1 == r0 && p.base == p.out ? 0 : MT * ((p.N + TN - 1) / TN);
-}
-
 // Whole CTA: prefix sums of the experts' tiles; returns their total.
-template <int PASS, int TN>
+template <typename C>
 __device__ int build_prefix(const GemmParams &p, GemmSmem &s, int MT) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.E + kThreads - 1) / kThreads, e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
+    const int per = (p.E + C::kThreads - 1) / C::kThreads, e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
     int sum = 0;
     for (int e = e0; e < e1; ++e) {
         int r0, r1;
         if (!range_of(p, e, r0, r1) && blockIdx.x == 0) flag(p.status, MOE_DEV_BAD_INDEX);
-        const int n = tiles_of<PASS, TN>(p, e, r0, r1, MT);
         s.prefix[e] = sum;
-        sum += n;
+        if (C::PASS != kWgrad) sum += MT * ((r1 - r0 + C::TN - 1) / C::TN);
+        // an expert without rows: nothing to do where the sum so far is in place
+        else if (r1 > r0 || p.base != p.out) sum += MT * ((p.N + C::TN - 1) / C::TN);
     }
     int incl = sum;
 #pragma unroll
@@ -117,7 +122,7 @@ __device__ int build_prefix(const GemmParams &p, GemmSmem &s, int MT) {
     if (lane == 31) s.warp_sum[warp] = incl;
     __syncthreads();
     int before = incl - sum, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < C::kThreads / 32; ++w) {
         if (w < warp) before += s.warp_sum[w];
         total += s.warp_sum[w];
     }
@@ -128,13 +133,14 @@ __device__ int build_prefix(const GemmParams &p, GemmSmem &s, int MT) {
 }
 
 struct Tile {
-    int e, m0;       // expert; first M index
+    int e, m0;       // expert; first M index of this CTA
     int c0, n;       // forward, dgrad: first sorted pair and pairs; wgrad: first n and their number
     int r0, r1;      // the expert's rows
+    int npad, b0;    // n padded to the MMA's 16; first of the npad / CG of them whose B rows this CTA loads
 };
 
-template <int PASS, int TN>
-__device__ __forceinline__ Tile tile_at(const GemmParams &p, const GemmSmem &s, int tau, int MT) {
+template <typename C>
+__device__ __forceinline__ Tile tile_at(const GemmParams &p, const GemmSmem &s, int tau, int MT, int rank) {
     int lo = 0, hi = p.E;  // last e with prefix[e] <= tau; experts without tiles share the next one's prefix
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -144,22 +150,24 @@ __device__ __forceinline__ Tile tile_at(const GemmParams &p, const GemmSmem &s, 
     t.e = lo;
     range_of(p, lo, t.r0, t.r1);
     const int local = tau - s.prefix[lo], j = local / MT;
-    t.m0 = (local - j * MT) * kTileM;
-    if (PASS == kWgrad) {
-        t.c0 = j * TN;
-        t.n = min(TN, p.N - t.c0);
+    t.m0 = ((local - j * MT) * C::CG + rank) * kTileM;
+    if (C::PASS == kWgrad) {
+        t.c0 = j * C::TN;
+        t.n = min(C::TN, p.N - t.c0);
     } else {  // the rows spread evenly over their tiles, in multiples of 16
-        const int rows = t.r1 - t.r0, nt = (rows + TN - 1) / TN;
+        const int rows = t.r1 - t.r0, nt = (rows + C::TN - 1) / C::TN;
         const int per = ((rows + nt - 1) / nt + 15) & ~15;
         t.c0 = t.r0 + j * per;
         t.n = min(per, t.r1 - t.c0);
     }
+    t.npad = (t.n + 15) & ~15;
+    t.b0 = rank * (t.npad / C::CG);
     return t;
 }
 
-template <int PASS>
+template <typename C>
 __device__ __forceinline__ int stages_of(const GemmParams &p, const Tile &t) {
-    return ((PASS == kWgrad ? t.r1 - t.r0 : p.I) + kTileI - 1) / kTileI;
+    return ((C::PASS == kWgrad ? t.r1 - t.r0 : p.I) + kTileI - 1) / kTileI;
 }
 
 // MN-major operand, 128-byte swizzle: blocks of 64 along MN 8192 bytes apart
@@ -169,283 +177,462 @@ __device__ __forceinline__ uint64_t desc_mn128(uint32_t saddr) {
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-// Token row of sorted pair `pair`, or a row past the tensor (which reads as
-// zeros) where the token or the pair is out of bounds.
-__device__ __forceinline__ int picked_row(const GemmParams &p, int pair, int end, int32_t *status) {
-    if (pair >= end) return p.rows_a;
-    if (!p.sorted_tok) return pair;
-    const int t = p.sorted_tok[pair];
-    if (t >= 0 && t < p.rows_a) return t;
-    flag(status, MOE_DEV_BAD_INDEX);
-    return p.rows_a;
-}
+// Position in the ring of stages.
+template <typename C>
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
 
-// Load warp: fills stage after stage, all tiles of this CTA in a row.
-template <int PASS, int TN>
-__device__ void load_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &m, unsigned char *dyn, int total, int MT) {
-    using C = Cfg<PASS, TN>;
-    const int lane = threadIdx.x & 31;
+// TMA warp: fills stage after stage, all tiles of this CTA in a row. The bytes
+// of both CTAs of a pair count on rank 0's barrier.
+template <typename C>
+__device__ void load_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &m, unsigned char *dyn, int total, int MT,
+                           int rank) {
+    Ring<C> at;
     int it = 0;
     bool ok = true;
-    for (int tau = blockIdx.x; tau < total && ok; tau += gridDim.x) {
-        const Tile t = tile_at<PASS, TN>(p, s, tau, MT);
-        const int KS = stages_of<PASS>(p, t);
-        const int ablocks = min(2, (p.M - t.m0 + 63) / 64);  // 64-wide blocks of an MN-major A inside the tensor
-        // forward by token: this lane's rows of N, four at a time (8 for 256 columns)
-        int pick[TN / 128 > 0 ? TN / 128 : 1][4];
-        if (PASS == kForward && p.sorted_tok) {
-#pragma unroll
-            for (int i = 0; i < (TN + 127) / 128; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    pick[i][r] = picked_row(p, t.c0 + 4 * (lane + 32 * i) + r, t.c0 + t.n, p.status);
-        }
-        for (int ks = 0; ks < KS; ++ks, ++it) {
-            const int stage = it % C::kStages;
-            if (!tc::mbar_wait(&s.empty[stage], ((it / C::kStages) & 1) ^ 1, kWaitNs) || s.abort) {
+    const uint32_t full0 = C::CG == 2 ? tc::at_rank(tc::smem_u32(&s.full[0]), 0) : tc::smem_u32(&s.full[0]);
+    const uint32_t dyn0 = tc::smem_u32(dyn);
+    auto load2 = [](uint32_t dst, const void *map, int x, int y, uint32_t bar) {
+        if (C::CG == 2) tc::tma_load_2d_pair(dst, map, x, y, bar);
+        else tc::tma_load_2d_at(dst, map, x, y, bar);
+    };
+    auto load3 = [](uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
+        if (C::CG == 2) tc::tma_load_3d_pair(dst, map, x, y, z, bar);
+        else tc::tma_load_3d_at(dst, map, x, y, z, bar);
+    };
+    for (int tau = blockIdx.x / C::CG; tau < total && ok; tau += gridDim.x / C::CG) {
+        const Tile t = tile_at<C>(p, s, tau, MT, rank);
+        const int KS = stages_of<C>(p, t);
+        // 64-wide blocks of an MN-major A that lie inside the tensor (none for a
+        // CTA whose rows all lie past it), and the same of both CTAs of a pair
+        const int ablocks = max(0, min(2, (p.M - t.m0 + 63) / 64));
+        const int ablocks_all = min(2 * C::CG, (p.M - (t.m0 - rank * kTileM) + 63) / 64);
+        // rows of B: boxes of 64, a short rest in boxes of 16 (the same in both CTAs)
+        const int brows = t.npad / C::CG, rest = brows & 63, brow0 = t.c0 + t.b0;
+        const int box64 = brows / 64 + (rest > 32), box16 = rest > 32 ? 0 : (rest + 15) / 16;
+        const int bblocks = (brows + 63) / 64;  // wgrad: 64-wide blocks of n
+        // bytes of a stage of both CTAs
+        const uint32_t bytes_a = C::PASS == kForward ? C::CG * C::kA : ablocks_all * 8192;
+        const uint32_t bytes_b = C::PASS == kWgrad ? C::CG * bblocks * 8192
+                                                   : C::PICK ? 0 : C::CG * (box64 * 8192 + box16 * 2048);
+        for (int ks = 0; ks < KS; ++ks, ++it, at.next()) {
+            if (!tc::mbar_wait_warp(&s.empty[at.stage], at.phase ^ 1, kWaitNs)) {
                 ok = false;
                 break;
             }
-            unsigned char *a = dyn + stage * C::kStage, *b = a + C::kA;
-            uint64_t *bar = &s.full[stage];
-            if (PASS != kWgrad) {
-                const bool small = t.n <= 48;
-                const bool by_token = PASS == kForward && p.sorted_tok;
-                const int picks = (t.n + 3) / 4, boxes = small ? (t.n + 15) / 16 : (t.n + 63) / 64;
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(bar, uint32_t((PASS == kForward ? C::kA : ablocks * 8192) +
-                                                            (by_token ? picks * 512 : boxes * (small ? 2048 : 8192))));
-                    if (PASS == kForward) {
-                        tc::tma_load_3d(a, &m.w, kTileI * ks, t.m0, t.e, bar);
-                    } else {
-                        for (int i = 0; i < ablocks; ++i)
-                            tc::tma_load_3d(a + 8192 * i, &m.w, t.m0 + 64 * i, kTileI * ks, t.e, bar);
-                    }
-                    if (!by_token)
-                        for (int i = 0; i < boxes; ++i)
-                            tc::tma_load_2d(b + i * (small ? 2048 : 8192), small ? &m.rows16 : &m.rows, kTileI * ks,
-                                            t.c0 + i * (small ? 16 : 64), bar);
-                }
-                __syncwarp();
-                if (by_token) {
+            const uint32_t a = dyn0 + at.stage * C::kStage, b = a + C::kA, bar = full0 + at.stage * 8;
+            const int i0 = kTileI * ks;
+            // wgrad's last stage of an expert, and its rows by token, come from the gathering warps
+            const bool load_b = C::PASS == kWgrad ? t.r1 - t.r0 - i0 >= kTileI : !C::PICK;
+            const bool load_a = C::PASS != kWgrad || (load_b && !p.sorted_tok);
+            if (tc::elect_one()) {
+                if (rank == 0)
+                    tc::mbar_arrive_expect_tx(&s.full[at.stage], (load_a ? bytes_a : 0) + (load_b ? bytes_b : 0));
+                if (C::PASS == kForward) {
+                    load3(a, &m.w, i0, t.m0, t.e, bar);
+                } else if (load_a) {
 #pragma unroll
-                    for (int i = 0; i < (TN + 127) / 128; ++i)
-                        if (lane + 32 * i < picks)
-                            tc::tma_gather4(b + (lane + 32 * i) * 512, &m.pick, kTileI * ks, pick[i][0], pick[i][1],
-                                            pick[i][2], pick[i][3], bar);
+                    for (int i = 0; i < 2; ++i)
+                        if (i < ablocks) {
+                            if (C::PASS == kDgrad) load3(a + 8192 * i, &m.w, t.m0 + 64 * i, i0, t.e, bar);
+                            else load2(a + 8192 * i, &m.rows, t.m0 + 64 * i, t.r0 + i0, bar);
+                        }
                 }
-            } else {
-                const int first = t.r0 + kTileI * ks, left = t.r1 - first;
-                const bool tail = left < kTileI;
-                const int bboxes = (t.n + 63) / 64;
-                const int picks = (tail ? (left + 15) & ~15 : kTileI) / 4;  // groups of four rows
-                const bool pick_a = tail || p.sorted_tok;
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(bar, uint32_t(ablocks * (pick_a ? picks * 512 : 8192) +
-                                                            (tail ? bboxes * picks * 512 : bboxes * 8192)));
-                    if (!pick_a)
-                        for (int i = 0; i < ablocks; ++i)
-                            tc::tma_load_2d(a + 8192 * i, &m.rows, t.m0 + 64 * i, first, bar);
-                    if (!tail)
-                        for (int i = 0; i < bboxes; ++i)
-                            tc::tma_load_2d(b + 8192 * i, &m.dy, t.c0 + 64 * i, first, bar);
-                }
-                __syncwarp();
-                if (pick_a) {  // lane: 64-column block lane / 16, rows 4 (lane % 16) ..
-                    const int g = lane & 15, blk = lane >> 4;
-                    if (g < picks && blk < ablocks) {
-                        int r[4];
+                if (C::PASS == kWgrad && load_b) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) r[i] = picked_row(p, first + 4 * g + i, t.r1, p.status);
-                        tc::tma_gather4(a + 8192 * blk + 512 * g, &m.pick, t.m0 + 64 * blk, r[0], r[1], r[2], r[3], bar);
-                    }
+                    for (int i = 0; i < C::kBRows / 64; ++i)
+                        if (i < bblocks) load2(b + 8192 * i, &m.dy, brow0 + 64 * i, t.r0 + i0, bar);
                 }
-                if (tail)
-                    for (int i = lane; i < bboxes * picks; i += 32) {
-                        const int blk = i / picks, g = i - blk * picks;
-                        int r[4];
+                if (C::PASS != kWgrad && !C::PICK) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) r[j] = first + 4 * g + j < t.r1 ? first + 4 * g + j : p.P;
-                        tc::tma_gather4(b + 8192 * blk + 512 * g, &m.dy_pick, t.c0 + 64 * blk, r[0], r[1], r[2], r[3],
-                                        bar);
-                    }
+                    for (int i = 0; i < C::kBRows / 64; ++i)
+                        if (i < box64) load2(b + 8192 * i, &m.rows, i0, brow0 + 64 * i, bar);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (i < box16)
+                            load2(b + box64 * 8192 + 2048 * i, &m.rows16, i0, brow0 + box64 * 64 + 16 * i, bar);
+                }
             }
+            __syncwarp();
         }
     }
     if (!ok) {
         stop(s, p.status);
         // no copy may land after this CTA's shared memory has another owner
-        for (int i = max(0, it - C::kStages); i < it; ++i)
-            tc::mbar_wait(&s.full[i % C::kStages], (i / C::kStages) & 1, kWaitNs);
+        if (rank == 0)
+            for (int i = max(0, it - C::kStages); i < it; ++i)
+                tc::mbar_wait(&s.full[i % C::kStages], (i / C::kStages) & 1, kWaitNs);
     }
 }
 
-template <int PASS, int TN>
-__device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, int total, int MT, uint32_t tmem) {
-    using C = Cfg<PASS, TN>;
-    constexpr bool kMnA = PASS != kForward, kMnB = PASS == kWgrad;
-    int it = 0, count = 0;
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// Token row of sorted pair `pair`, -1 (read as zeros) where the pair or its token is out of bounds.
+__device__ __forceinline__ int picked_row(const GemmParams &p, int pair, int end) {
+    if (pair >= end) return -1;
+    if (!p.sorted_tok) return pair;
+    const int t = p.sorted_tok[pair];
+    if (t >= 0 && t < p.rows_a) return t;
+    flag(p.status, MOE_DEV_BAD_INDEX);
+    return -1;
+}
+
+// Gathering warps: forward's rows by token (K-major B); wgrad's rows by token
+// (MN-major A) and, in an expert's last stage, the rows of both operands. A
+// warp fills every fourth stage alone: it issues the whole stage, waits until
+// that has landed, makes it visible to the tensor cores and arrives on rank 0's
+// barrier. (With all four warps on each stage, a stage could be handed over only
+// after later ones were issued, which left half of the ring in flight.)
+template <typename C>
+__device__ void gather_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn, int total, int MT, int rank) {
+    const int warp = (threadIdx.x >> 5) - kPickWarp0, lane = threadIdx.x & 31;
+    const uint32_t full0 = C::CG == 2 ? tc::at_rank(tc::smem_u32(&s.full[0]), 0) : tc::smem_u32(&s.full[0]);
+    const uint32_t dyn0 = tc::smem_u32(dyn);
+    Ring<C> at;
+    int it = 0;
     bool ok = true;
-    for (int tau = blockIdx.x; tau < total && ok && !s.abort; tau += gridDim.x) {
-        const Tile t = tile_at<PASS, TN>(p, s, tau, MT);
-        const int KS = stages_of<PASS>(p, t);
+    for (int tau = blockIdx.x / C::CG; tau < total && ok; tau += gridDim.x / C::CG) {
+        const Tile t = tile_at<C>(p, s, tau, MT, rank);
+        const int KS = stages_of<C>(p, t), brows = t.npad / C::CG;
+        constexpr int kIdx = (C::kBRows + 31) / 32;
+        int idx[kIdx];  // forward: token rows of B rows lane + 32 i
+        if (C::PASS == kForward) {
+#pragma unroll
+            for (int i = 0; i < kIdx; ++i) {
+                const int r = lane + 32 * i;
+                idx[i] = r < brows ? picked_row(p, t.c0 + t.b0 + r, t.c0 + t.n) : -1;
+            }
+        }
+        for (int ks = 0; ks < KS; ++ks, ++it, at.next()) {
+            if (it % kPickWarps != warp) continue;
+            if (!tc::mbar_wait_warp(&s.empty[at.stage], at.phase ^ 1, kWaitNs)) {
+                ok = false;
+                break;
+            }
+            const uint32_t a = dyn0 + at.stage * C::kStage, b = a + C::kA;
+            if (C::PASS == kForward) {  // lane: chunk lane % 8 of rows lane / 8 + 4 i
+                const int ch = lane & 7, k = kTileI * ks + 8 * ch;
+                const uint16_t *from = p.rows + k;
+#pragma unroll
+                for (int i = 0; i < C::kBRows / 4; ++i) {
+                    const int r = (lane >> 3) + 4 * i;
+                    if (4 * i >= brows) break;
+                    const int row = __shfl_sync(0xffffffffu, idx[i / 8], r & 31);
+                    const bool in = row >= 0 && k < p.I;
+                    if (r < brows)
+                        cp_async16_or_zero(b + r * 128 + ((ch ^ (r & 7)) << 4),
+                                           in ? from + int64_t(row) * p.I : p.rows, in);
+                }
+            } else {
+                const int first = t.r0 + kTileI * ks, left = t.r1 - first;
+                const bool tail = left < kTileI;
+                const int rows = tail ? (left + 15) & ~15 : kTileI;
+                const int ch = lane & 15;  // lane: chunk lane % 16 of rows lane / 16 + 2 i
+                const uint32_t off = (ch >> 3) * 8192;
+                if (tail || p.sorted_tok) {
+                    const int m = t.m0 + 8 * ch;
+                    const uint16_t *from = p.rows + m;
+                    int row2[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) row2[i] = picked_row(p, first + lane + 32 * i, t.r1);
+#pragma unroll
+                    for (int i = 0; i < kTileI / 2; ++i) {
+                        const int r = (lane >> 4) + 2 * i;
+                        if (2 * i >= rows) break;
+                        const int row = __shfl_sync(0xffffffffu, row2[i / 16], r & 31);
+                        const bool in = row >= 0 && m < p.M;
+                        cp_async16_or_zero(a + off + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                                           in ? from + int64_t(row) * p.M : p.rows, in);
+                    }
+                }
+                if (tail) {
+                    static_assert(C::PASS != kWgrad || C::kBRows == 128, "16 chunks a row");
+                    const int n = t.c0 + t.b0 + 8 * ch;
+                    const uint16_t *from = p.dy + int64_t(first) * p.N + n;
+#pragma unroll 8
+                    for (int r = lane >> 4; r < rows; r += 2) {
+                        const bool in = r < left && n < p.N;
+                        cp_async16_or_zero(b + off + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                                           in ? from + int64_t(r) * p.N : p.dy, in);
+                    }
+                }
+            }
+            tc::cp_async_wait_all();
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(full0 + at.stage * 8);
+            __syncwarp();
+        }
+    }
+    if (!ok) stop(s, p.status);
+}
+
+template <typename C>
+__device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, int total, int MT, uint32_t tmem) {
+    constexpr bool kMnA = C::PASS != kForward, kMnB = C::PASS == kWgrad;
+    // descriptors advance by 16 of the contracted index: 32 bytes in a K-major row, 16 rows of an MN-major block
+    constexpr uint64_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
+    const uint32_t dyn0 = tc::smem_u32(dyn);
+    const uint64_t a0 = kMnA ? desc_mn128(dyn0) : tc::desc_sw128(dyn0);
+    const uint64_t b0 = kMnB ? desc_mn128(dyn0 + C::kA) : tc::desc_sw128(dyn0 + C::kA);
+    const uint32_t fmt = p.bf16 ? 1u : 0u;
+    const uint32_t idesc0 = tc::idesc_f16(kTileM * C::CG, 0) | (fmt << 7) | (fmt << 10) | (kMnA ? 1u << 15 : 0u) |
+                            (kMnB ? 1u << 16 : 0u);
+    auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+        if (C::CG == 2) tc::mma_f16_pair(d, a, b, idesc, acc);
+        else tc::mma_f16(d, a, b, idesc, acc);
+    };
+    auto commit = [](uint64_t *bar) {
+        if (C::CG == 2) tc::mma_commit_pair(bar);
+        else tc::mma_commit(bar);
+    };
+    Ring<C> at;
+    int count = 0;
+    bool ok = true;
+    for (int tau = blockIdx.x / C::CG; tau < total && ok && !s.abort; tau += gridDim.x / C::CG) {
+        const Tile t = tile_at<C>(p, s, tau, MT, 0);
+        const int KS = stages_of<C>(p, t);
         if (KS == 0) continue;  // wgrad of an expert without rows
         const int buf = count & 1;
-        if (!tc::mbar_wait(&s.tempty[buf], ((count >> 1) & 1) ^ 1, kWaitNs)) {
+        if (!tc::mbar_wait_warp(&s.tempty[buf], ((count >> 1) & 1) ^ 1, kWaitNs)) {
             ok = false;
             break;
         }
         tc::fence_after();
         ++count;
-        const uint32_t fmt = p.bf16 ? 1u : 0u;
-        const uint32_t idesc = tc::idesc_f16(kTileM, (t.n + 15) & ~15) | (fmt << 7) | (fmt << 10) |
-                               (kMnA ? 1u << 15 : 0u) | (kMnB ? 1u << 16 : 0u);
-        const uint32_t d = tmem + uint32_t(buf * TN);
-        for (int ks = 0; ks < KS; ++ks, ++it) {
-            const int stage = it % C::kStages;
-            if (!tc::mbar_wait(&s.full[stage], (it / C::kStages) & 1, kWaitNs)) {
+        const uint32_t idesc = idesc0 | (uint32_t(t.npad >> 3) << 17);
+        const uint32_t d = tmem + uint32_t(buf * C::TN);
+        int left = C::PASS == kWgrad ? t.r1 - t.r0 : p.I;
+        for (int ks = 0; ks < KS; ++ks, left -= kTileI, at.next()) {
+            if (!tc::mbar_wait_warp(&s.full[at.stage], at.phase, kWaitNs)) {
                 ok = false;
                 break;
             }
             tc::fence_after();
-            const uint32_t a = tc::smem_u32(dyn + stage * C::kStage), b = a + C::kA;
-            const int left = PASS == kWgrad ? t.r1 - t.r0 - kTileI * ks : p.I - kTileI * ks;
-            const int steps = min(4, (left + 15) >> 4);  // of 16; the last one reads zeros past the end
-            for (int kk = 0; kk < steps; ++kk)
-                tc::mma_f16(d, kMnA ? desc_mn128(a + 2048 * kk) : tc::desc_sw128(a + 32 * kk),
-                            kMnB ? desc_mn128(b + 2048 * kk) : tc::desc_sw128(b + 32 * kk), idesc, (ks | kk) ? 1u : 0u);
-            tc::mma_commit(&s.empty[stage]);
+            const uint64_t a = a0 + uint32_t(at.stage * (C::kStage >> 4)), b = b0 + uint32_t(at.stage * (C::kStage >> 4));
+            if (tc::elect_one()) {
+                // steps of 16; the last one reads zeros past the end
+                mma(d, a, b, idesc, ks ? 1u : 0u);
+                if (left > 16) mma(d, a + kStepA, b + kStepB, idesc, 1u);
+                if (left > 32) mma(d, a + 2 * kStepA, b + 2 * kStepB, idesc, 1u);
+                if (left > 48) mma(d, a + 3 * kStepA, b + 3 * kStepB, idesc, 1u);
+                commit(&s.empty[at.stage]);
+                if (ks == KS - 1) commit(&s.tfull[buf]);
+            }
+            __syncwarp();
         }
-        if (ok) tc::mma_commit(&s.tfull[buf]);
     }
     if (!ok) stop(s, p.status);
 }
 
-// Output element types behind one store: O a column's 32 consecutive values,
-// or, for 16-bit outputs, two columns at once (lane pairs swap halves so that
-// each lane holds two neighbours of one column).
-template <int PASS, int TN, typename O>
-__device__ void store_tiles(const GemmParams &p, GemmSmem &s, int total, int MT, uint32_t tmem) {
+// 32 x 32 accumulators (lanes M, columns) to 16-bit rows of 32 M values: loaded
+// as mma fragments, packed along the columns, turned by the transposing matrix
+// store into this warp's 2 KB ([column][32], 16-byte chunks swizzled against
+// bank conflicts), read back and written as 16-byte pieces.
+template <typename O>
+__device__ __forceinline__ void turn_and_store(uint32_t td, bool sums, uint32_t turn, O *out, int64_t pitch, int cols,
+                                               int m_left) {
+    const int lane = threadIdx.x & 31;
+    uint32_t v[2][16];
+    if (sums) {
+        tc::tmem_ld16x256_x4_nowait(td, v[0]);
+        tc::tmem_ld16x256_x4_nowait(td + (16u << 16), v[1]);
+        tc::tmem_ld_wait();
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0u;
+    }
+    __syncwarp();  // the chunks of the last 32 columns have been read
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float lo = __uint_as_float(v[j >> 1][4 * i + 2 * (j & 1)]);
+            const float hi = __uint_as_float(v[j >> 1][4 * i + 2 * (j & 1) + 1]);
+            const O pair[2] = {from_f32<O>(lo), from_f32<O>(hi)};
+            w[j] = *reinterpret_cast<const uint32_t *>(pair);
+        }
+        const int n = 8 * i + (lane & 7), ch = lane >> 3;
+        tc::stmatrix_x4_trans(turn + n * 64 + ((ch ^ ((n >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    const int ch = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = 8 * i + (lane >> 2);
+        uint4 r;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                     : "r"(turn + n * 64 + ((ch ^ ((n >> 1) & 3)) << 4)));
+        if (n < cols && 8 * ch < m_left) *reinterpret_cast<uint4 *>(out + n * pitch + 8 * ch) = r;
+    }
+}
+
+// Epilogue warps: lane quadrant warp % 4 of tensor memory, every second 32
+// columns. 16-bit output goes through turn_and_store; fp32 output as a column's
+// 32 consecutive values at a time. With a sum so far (wgrad), 16-bit output is
+// rounded only after the addition: two columns at once (lane pairs swap values
+// so that each lane holds two neighbours of one column), the sum read 32 columns
+// ahead of its use, the first 32 while the products still run.
+template <typename C, typename O>
+__device__ void store_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn, int total, int MT, uint32_t tmem,
+                            int rank) {
+    constexpr bool kAdd = C::PASS == kWgrad, kWide = sizeof(O) == 4;
+    constexpr int kVals = kWide ? 32 : 16;  // 32-bit words a lane stores of 32 columns
     const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = threadIdx.x & 31;
-    const int q = (warp + kEpiWarp0) & 3, half = warp >> 2;  // lane quadrant of tensor memory; column half
+    const int q = (warp + kEpiWarp0) & 3, half = warp >> 2, odd = lane & 1;
+    const uint32_t turn = tc::smem_u32(dyn) + C::kStages * C::kStage + warp * kTurn;
     int count = 0;
-    for (int tau = blockIdx.x; tau < total && !s.abort; tau += gridDim.x) {
-        const Tile t = tile_at<PASS, TN>(p, s, tau, MT);
-        const bool sums = stages_of<PASS>(p, t) > 0;
+    for (int tau = blockIdx.x / C::CG; tau < total && !s.abort; tau += gridDim.x / C::CG) {
+        const Tile t = tile_at<C>(p, s, tau, MT, rank);
+        const bool sums = stages_of<C>(p, t) > 0;
+        const int m = t.m0 + 32 * q + lane;
+        const bool in = m < p.M;
+        const int64_t row0 = C::PASS == kWgrad ? int64_t(t.e) * p.N + t.c0 : int64_t(t.c0);
+        // word i of 32 columns from c: fp32 column c + i; 16 bits column c + 2 i + odd, elements m & ~1 and next
+        const int64_t at0 = kWide ? row0 * p.M + m : (row0 + odd) * p.M + (m & ~1);
+        const int step = kWide ? 1 : 2, first = kWide ? 0 : odd;
+        uint32_t old[kAdd ? kVals : 1];
+        auto read_old = [&](int c) {
+            const O *b = static_cast<const O *>(p.base) + at0 + int64_t(c) * p.M;
+#pragma unroll
+            for (int i = 0; i < kVals; ++i)
+                old[kAdd ? i : 0] = in && c + step * i + first < t.n
+                                        ? *reinterpret_cast<const uint32_t *>(b + int64_t(step * i) * p.M) : 0u;
+        };
+        if (kAdd && p.base && 32 * half < t.n) read_old(32 * half);
         const int buf = count & 1;
         if (sums) {
-            if (!tc::mbar_wait_sleep(&s.tfull[buf], (count >> 1) & 1, kWaitNs, 64)) {
+            if (!tc::mbar_wait_sleep(&s.tfull[buf], (count >> 1) & 1, kWaitNs, 32)) {
                 stop(s, p.status);
                 break;
             }
             tc::fence_after();
             ++count;
         }
-        const int m = t.m0 + 32 * q + lane;
-        const int64_t row0 = PASS == kWgrad ? int64_t(t.e) * p.N + t.c0 : int64_t(t.c0);
-        const uint32_t td = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * TN);
-        for (int c = 16 * half; c < t.n; c += 32) {
-            float v[16];
+        const uint32_t td = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * C::TN);
+        for (int c = 32 * half; c < t.n; c += 64) {
+            if constexpr (!kWide)
+                if (!(kAdd && p.base)) {
+                    const int m1 = t.m0 + 32 * q;
+                    turn_and_store<O>(td + c, sums, turn, static_cast<O *>(p.out) + (row0 + c) * p.M + m1, p.M,
+                                      t.n - c, p.M - m1);
+                    continue;
+                }
+            uint32_t v[32];
             if (sums) {
-                tc::tmem_ld16(td + c, v);
+                tc::tmem_ld32_nowait(td + c, v);
+                tc::tmem_ld_wait();
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                for (int i = 0; i < 32; ++i) v[i] = 0u;
             }
-            if (sizeof(O) == 4) {
-                if (m < p.M) {
-                    float *o = static_cast<float *>(p.out) + (row0 + c) * p.M + m;
-                    if (PASS == kWgrad && p.base) {
-                        const float *b = static_cast<const float *>(p.base) + (row0 + c) * p.M + m;
-                        float bv[16];
+            uint32_t word[kVals];
+            if (kWide) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) bv[j] = c + j < t.n ? b[int64_t(j) * p.M] : 0.f;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] += bv[j];
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c + j < t.n) o[int64_t(j) * p.M] = v[j];
+                for (int i = 0; i < kVals; ++i) {
+                    word[i] = v[i];
+                    if (kAdd && p.base)
+                        word[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(old[kAdd ? i : 0]));
                 }
             } else {
-                const int odd = lane & 1;
-                const int64_t at = (row0 + c + odd) * p.M + (m & ~1);
-                uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<O *>(p.out) + at);
-                const uint32_t *b = reinterpret_cast<const uint32_t *>(static_cast<const O *>(p.base) + at);
-                uint32_t bv[8];
-                if (PASS == kWgrad && p.base) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        bv[j] = m < p.M && c + 2 * j + odd < t.n ? b[int64_t(j) * p.M] : 0u;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * j] : v[2 * j + 1], 1);
-                    float lo = odd ? got : v[2 * j], hi = odd ? v[2 * j + 1] : got;
-                    O pair[2];
-                    if (PASS == kWgrad && p.base) {
-                        const O *old = reinterpret_cast<const O *>(&bv[j]);
-                        lo += to_f32(old[0]);
-                        hi += to_f32(old[1]);
+                for (int i = 0; i < kVals; ++i) {
+                    const uint32_t mine = odd ? v[(2 * i + 1) & 31] : v[(2 * i) & 31];
+                    const uint32_t got =
+                        __shfl_xor_sync(0xffffffffu, odd ? v[(2 * i) & 31] : v[(2 * i + 1) & 31], 1);
+                    float lo = __uint_as_float(odd ? got : mine), hi = __uint_as_float(odd ? mine : got);
+                    if (kAdd && p.base) {
+                        const O *o = reinterpret_cast<const O *>(&old[kAdd ? i : 0]);
+                        lo += to_f32(o[0]);
+                        hi += to_f32(o[1]);
                     }
-                    pair[0] = from_f32<O>(lo);
-                    pair[1] = from_f32<O>(hi);
-                    if (m < p.M && c + 2 * j + odd < t.n) o[int64_t(j) * p.M] = *reinterpret_cast<const uint32_t *>(pair);
+                    O pair[2] = {from_f32<O>(lo), from_f32<O>(hi)};
+                    word[i] = *reinterpret_cast<const uint32_t *>(pair);
                 }
             }
+            if (kAdd && p.base && c + 64 < t.n) read_old(c + 64);
+            O *o = static_cast<O *>(p.out) + at0 + int64_t(c) * p.M;
+#pragma unroll
+            for (int i = 0; i < kVals; ++i)
+                if (in && c + step * i + first < t.n)
+                    *reinterpret_cast<uint32_t *>(o + int64_t(step * i) * p.M) = word[i];
         }
         if (sums) {
             tc::fence_before();
-            tc::mbar_arrive(&s.tempty[buf]);
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t bar = tc::smem_u32(&s.tempty[buf]);
+                tc::mbar_arrive_cluster(C::CG == 2 ? tc::at_rank(bar, 0) : bar);
+            }
         }
     }
 }
 
-template <int PASS, int TN>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename C>
+__global__ void __launch_bounds__(C::kThreads, 1)
     expert_gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ GemmMaps maps) {
-    using C = Cfg<PASS, TN>;
     extern __shared__ __align__(1024) unsigned char dyn_raw[];
     unsigned char *dyn =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
     __shared__ GemmSmem s;
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int MT = (p.M + kTileM - 1) / kTileM;
-    constexpr int kCols = 2 * TN < 32 ? 32 : 2 * TN;
+    const int rank = C::CG == 2 ? int(tc::cluster_rank()) : 0;
+    const int MT = (p.M + kTileM * C::CG - 1) / (kTileM * C::CG);
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            tc::mbar_init(&s.full[i], 1);
+            tc::mbar_init(&s.full[i], 1 + (C::PICK ? C::CG : 0));
             tc::mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s.tfull[i], 1);
-            tc::mbar_init(&s.tempty[i], 32 * kEpiWarps);
+            tc::mbar_init(&s.tempty[i], C::CG * kEpiWarps);
         }
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem_base, kCols);
-    const int total = build_prefix<PASS, TN>(p, s, MT);
+    if (warp == kMmaWarp) {
+        if (C::CG == 2) tc::tmem_alloc_pair(&s.tmem_base, C::kCols);
+        else tc::tmem_alloc(&s.tmem_base, C::kCols);
+    }
+    const int total = build_prefix<C>(p, s, MT);
     tc::fence_before();
-    __syncthreads();
+    if (C::CG == 2) tc::cluster_sync();  // both CTAs' barriers are set up
+    else __syncthreads();
     tc::fence_after();
     const uint32_t tmem = s.tmem_base;
     if (warp == kLoadWarp) {
-        load_tiles<PASS, TN>(p, s, maps, dyn, total, MT);
+        load_tiles<C>(p, s, maps, dyn, total, MT, rank);
     } else if (warp == kMmaWarp) {
-        if ((tid & 31) == 0) issue_mma<PASS, TN>(p, s, dyn, total, MT, tmem);
+        if (rank == 0) issue_mma<C>(p, s, dyn, total, MT, tmem);
+    } else if (warp >= kPickWarp0) {
+        if (C::PICK) gather_tiles<C>(p, s, dyn, total, MT, rank);
     } else if (p.out_fp32) {
-        store_tiles<PASS, TN, float>(p, s, total, MT, tmem);
+        store_tiles<C, float>(p, s, dyn, total, MT, tmem, rank);
     } else if (p.bf16) {
-        store_tiles<PASS, TN, __nv_bfloat16>(p, s, total, MT, tmem);
+        store_tiles<C, __nv_bfloat16>(p, s, dyn, total, MT, tmem, rank);
     } else {
-        store_tiles<PASS, TN, __half>(p, s, total, MT, tmem);
+        store_tiles<C, __half>(p, s, dyn, total, MT, tmem, rank);
     }
+    __syncwarp();
     tc::fence_before();
-    __syncthreads();
+    if (C::CG == 2) tc::cluster_sync();  // neither leaves while the other's products or arrivals may reach it
+    else __syncthreads();
     if (warp == kMmaWarp) {
         tc::fence_after();
-        tc::tmem_dealloc(tmem, kCols);
+        if (C::CG == 2) tc::tmem_dealloc_pair(tmem, C::kCols);
+        else tc::tmem_dealloc(tmem, C::kCols);
     }
 }
 
@@ -486,54 +673,66 @@ bool map16(CUtensorMap *m, bool bf16, const void *base, int64_t inner, int64_t r
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int PASS, int TN>
+template <typename C>
 moe_status launch(const GemmParams &p, const GemmMaps &maps, int64_t most_tiles, int sms, cudaStream_t stream) {
-    using C = Cfg<PASS, TN>;
-    static_assert(C::kStages >= 4, "fewer than four stages fit");
-    if (cudaFuncSetAttribute(expert_gemm_kernel<PASS, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
+    if (cudaFuncSetAttribute(expert_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
         cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
-    const int grid = int(std::min<int64_t>(sms, most_tiles));
-    expert_gemm_kernel<PASS, TN><<<grid, kThreads, C::kSmem, stream>>>(p, maps);
-    return launch_status();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(sms / C::CG, most_tiles)) * C::CG);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = C::CG;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = C::CG > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, expert_gemm_kernel<C>, p, maps) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
 }
 
-// rows: a (forward, wgrad) or dy (dgrad); inner: its row length.
-moe_status run_gemm(int pass, GemmParams &p, const void *w, const void *rows, const void *dy, int N, int K,
-                    cudaStream_t stream) {
+// rows: a (forward, wgrad) or dy (dgrad).
+moe_status run_gemm(int pass, GemmParams &p, const void *w, int N, int K, cudaStream_t stream) {
     int sms = 0;
     if (!host_setup(sms)) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
     GemmMaps maps = {};
-    const bool bf = p.bf16;
+    const bool bf = p.bf16, pick = p.sorted_tok != nullptr;
     const int inner = pass == kDgrad ? N : K;
-    // an empty batch (wgrad) has no rows to describe; nothing is loaded then
-    const int64_t nrows = std::max(p.rows_a, 1), npairs = std::max(p.P, 1);
     bool ok = true;
-    if (p.P > 0) {
-        ok = map16(&maps.rows, bf, rows, inner, nrows, 0, 64) && map16(&maps.pick, bf, rows, inner, nrows, 0, 1);
-        if (pass != kWgrad)
-            ok = ok && map16(&maps.rows16, bf, rows, inner, nrows, 0, 16) &&
-                 map16(&maps.w, bf, w, K, N, p.E, pass == kForward ? 128 : 64);
-        else
-            ok = ok && map16(&maps.dy, bf, dy, N, npairs, 0, 64) && map16(&maps.dy_pick, bf, dy, N, npairs, 0, 1);
+    if (p.P > 0) {  // an empty batch (wgrad) has no rows to describe, and loads none
+        if (!pick)
+            ok = map16(&maps.rows, bf, p.rows, inner, p.rows_a, 0, 64) &&
+                 (pass == kWgrad || map16(&maps.rows16, bf, p.rows, inner, p.rows_a, 0, 16));
+        if (pass == kWgrad) ok = ok && map16(&maps.dy, bf, p.dy, N, p.P, 0, 64);
+        else ok = ok && map16(&maps.w, bf, w, K, N, p.E, pass == kForward ? 128 : 64);
     }
     if (!ok) return MOE_ERR_CUDA;
-    const int64_t MT = (p.M + kTileM - 1) / kTileM;
+    const int64_t MT1 = (p.M + kTileM - 1) / kTileM, MT2 = (MT1 + 1) / 2;
     if (pass == kWgrad)
-        return launch<kWgrad, 256>(p, maps, MT * ((N + 255) / 256) * p.E, sms, stream);
-    // Few rows an expert: narrow tiles, so that more stages of weights are in flight.
+        return launch<Cfg<kWgrad, 2, 256, true>>(p, maps, MT2 * ((N + 255) / 256) * p.E, sms, stream);
+    // Few rows an expert: the weights' bytes bound the call, so tiles are narrow
+    // and single, with more stages of weights in flight and more of them.
     const int64_t experts = std::min<int64_t>(p.E, p.P);
-    const bool narrow = p.P <= 16 * experts;
-    const int64_t most = MT * (experts + p.P / (narrow ? 32 : 256));
-    if (pass == kForward)
-        return narrow ? launch<kForward, 32>(p, maps, most, sms, stream)
-                      : launch<kForward, 256>(p, maps, most, sms, stream);
-    return narrow ? launch<kDgrad, 32>(p, maps, most, sms, stream) : launch<kDgrad, 256>(p, maps, most, sms, stream);
+    if (p.P <= 16 * experts) {
+        const int64_t most = MT1 * (experts + p.P / 32);
+        if (pass == kDgrad) return launch<Cfg<kDgrad, 1, 32, false>>(p, maps, most, sms, stream);
+        return pick ? launch<Cfg<kForward, 1, 32, true>>(p, maps, most, sms, stream)
+                    : launch<Cfg<kForward, 1, 32, false>>(p, maps, most, sms, stream);
+    }
+    const int64_t most = MT2 * (experts + p.P / 256);
+    if (pass == kDgrad) return launch<Cfg<kDgrad, 2, 256, false>>(p, maps, most, sms, stream);
+    return pick ? launch<Cfg<kForward, 2, 256, true>>(p, maps, most, sms, stream)
+                : launch<Cfg<kForward, 2, 256, false>>(p, maps, most, sms, stream);
 }
 
 moe_status check_gemm(int dtype, int T, int E, int k, int N, int K, int out_dtype) {
@@ -556,9 +755,9 @@ MOE_API moe_status moe_expert_gemm(const void *a, const void *W, int dtype, int 
     const moe_status st = check_gemm(dtype, T, E, k, N, K, out_dtype);
     if (st != MOE_OK || T == 0) return st;
     if (!a || !W || !offsets || !out || !aligned16(a) || !aligned16(W) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
-    GemmParams p = {offsets, sorted_tok, nullptr, out, sorted_tok ? T : T * k, T * k, E, N, K, 0,
-                    dtype == MOE_BF16, out_dtype == MOE_FP32, dev_status};
-    return run_gemm(kForward, p, W, a, nullptr, N, K, as_cuda(stream));
+    GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), nullptr, nullptr, out,
+                    sorted_tok ? T : T * k, T * k, E, N, K, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, dev_status};
+    return run_gemm(kForward, p, W, N, K, as_cuda(stream));
 }
 
 MOE_API moe_status moe_expert_gemm_dgrad(const void *dy, const void *W, int dtype, int T, int E, int k, int N, int K,
@@ -567,9 +766,9 @@ MOE_API moe_status moe_expert_gemm_dgrad(const void *dy, const void *W, int dtyp
     const moe_status st = check_gemm(dtype, T, E, k, N, K, out_dtype);
     if (st != MOE_OK || T == 0) return st;
     if (!dy || !W || !offsets || !da || !aligned16(dy) || !aligned16(W) || !aligned16(da)) return MOE_ERR_INVALID_ARG;
-    GemmParams p = {offsets, nullptr, nullptr, da, T * k, T * k, E, K, N, 0,
-                    dtype == MOE_BF16, out_dtype == MOE_FP32, dev_status};
-    return run_gemm(kDgrad, p, W, dy, nullptr, N, K, as_cuda(stream));
+    GemmParams p = {offsets, nullptr, static_cast<const uint16_t *>(dy), nullptr, nullptr, da,
+                    T * k, T * k, E, K, N, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, dev_status};
+    return run_gemm(kDgrad, p, W, N, K, as_cuda(stream));
 }
 
 MOE_API moe_status moe_expert_gemm_wgrad(const void *dy, const void *a, int dtype, int T, int E, int k, int N, int K,
@@ -579,7 +778,7 @@ MOE_API moe_status moe_expert_gemm_wgrad(const void *dy, const void *a, int dtyp
     if (st != MOE_OK) return st;
     if (!offsets || !dW || !aligned16(dW) || !aligned16(base)) return MOE_ERR_INVALID_ARG;
     if (T > 0 && (!dy || !a || !aligned16(dy) || !aligned16(a))) return MOE_ERR_INVALID_ARG;
-    GemmParams p = {offsets, sorted_tok, base, dW, sorted_tok ? T : T * k, T * k, E, K, 0, N,
-                    dtype == MOE_BF16, out_dtype == MOE_FP32, dev_status};
-    return run_gemm(kWgrad, p, nullptr, a, dy, N, K, as_cuda(stream));
+    GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), static_cast<const uint16_t *>(dy), base, dW,
+                    sorted_tok ? T : T * k, T * k, E, K, 0, N, dtype == MOE_BF16, out_dtype == MOE_FP32, dev_status};
+    return run_gemm(kWgrad, p, nullptr, N, K, as_cuda(stream));
 }
