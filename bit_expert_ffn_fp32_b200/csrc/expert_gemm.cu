@@ -14,12 +14,12 @@
 //   wgrad    k     n       pairs        a rows, MN-major       dy rows, MN-major
 // Wide tiles are computed by pairs of CTAs (cta_group::2, M = 256): each loads
 // its own half of A and of B, which cuts the L2 traffic of a 160-row tile by a
-// quarter and is what bounds experts of that size. Operands come by TMA in the
-// 128-byte swizzle, except rows picked by token and wgrad's last stage of an
-// expert (rows past its end must read as zeros there, as they are summed):
-// those are written by four warps with 16-byte cp.async in the same swizzle
-// (gathering TMA loads of four rows took about 48 cycles each, ten bytes a
-// cycle). Warps: TMA, MMA issue, eight for the epilogue, four that gather; two
+// quarter. Operands come by TMA in the 128-byte swizzle, except rows picked by
+// token and wgrad's last stage of an expert (rows past its end must read as
+// zeros there, as they are summed): those are written by gathering warps with
+// 16-byte cp.async in the same swizzle (gathering TMA loads of four rows took
+// about 48 cycles each, ten bytes a cycle). Warps: TMA, MMA issue, eight for
+// the epilogue, eight that gather and one that hands their stages on; two
 // accumulators, so that the epilogue of one tile runs beside the products of
 // the next. Every wait is bounded and sets MOE_DEV_TIMEOUT.
 #include <cuda.h>
@@ -39,7 +39,9 @@ enum Pass { kForward = 0, kDgrad = 1, kWgrad = 2 };
 constexpr int kTileM = 128;      // rows of tensor memory of a CTA
 constexpr int kTileI = 64;       // contracted index a stage: 128 bytes, one swizzle row
 constexpr int kLoadWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 8, kPickWarp0 = kEpiWarp0 + kEpiWarps;
-constexpr int kPickWarps = 4;    // each gathers every fourth stage
+constexpr int kPickWarps = 8, kPickGroups = 2;  // gathering warps; stages they fill at the same time
+constexpr int kPickThreads = 32 * kPickWarps / kPickGroups;
+constexpr int kRelayWarp = kPickWarp0 + kPickWarps;
 constexpr int kMaxStages = 10;
 constexpr int kTurn = 2048;      // per epilogue warp: 32 x 32 16-bit values on their way to 16-byte stores
 constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
@@ -64,10 +66,10 @@ struct GemmMaps {
 };
 
 struct GemmSmem {
-    uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+    uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages], tfull[2], tempty[2];
     uint32_t tmem_base;
     int abort;
-    int warp_sum[kPickWarp0 + kPickWarps];
+    int warp_sum[kRelayWarp + 1];
     int prefix[kMaxE + 1];  // tiles before expert e
 };
 
@@ -76,7 +78,7 @@ template <int PASS_, int CG_, int TN_, bool PICK_>
 struct Cfg {
     static constexpr int PASS = PASS_, CG = CG_, TN = TN_;
     static constexpr bool PICK = PICK_;
-    static constexpr int kThreads = 32 * (PICK ? kPickWarp0 + kPickWarps : kPickWarp0);
+    static constexpr int kThreads = 32 * (PICK ? kRelayWarp + 1 : kPickWarp0);
     static constexpr int kBRows = TN / CG;  // of B a CTA holds
     static constexpr int kA = kTileM * 128, kB = kBRows * 128, kStage = kA + kB;
     // what fits beside the tables in 227 KB
@@ -288,89 +290,112 @@ __device__ __forceinline__ int picked_row(const GemmParams &p, int pair, int end
 }
 
 // Gathering warps: forward's rows by token (K-major B); wgrad's rows by token
-// (MN-major A) and, in an expert's last stage, the rows of both operands. A
-// warp fills every fourth stage alone: it issues the whole stage, waits until
-// that has landed, makes it visible to the tensor cores and arrives on rank 0's
-// barrier. (With all four warps on each stage, a stage could be handed over only
-// after later ones were issued, which left half of the ring in flight.)
+// (MN-major A) and, in an expert's last stage, the rows of both operands. Four
+// warps fill a stage, the two groups of four every second one. They never wait
+// for their copies: those arrive on `landed` by themselves, so that a whole ring
+// of stages is in flight, and the relay warp hands the stage to the MMA.
 template <typename C>
 __device__ void gather_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn, int total, int MT, int rank) {
-    const int warp = (threadIdx.x >> 5) - kPickWarp0, lane = threadIdx.x & 31;
-    const uint32_t full0 = C::CG == 2 ? tc::at_rank(tc::smem_u32(&s.full[0]), 0) : tc::smem_u32(&s.full[0]);
+    const int tid = (threadIdx.x - 32 * kPickWarp0) % kPickThreads;
+    const int group = (threadIdx.x - 32 * kPickWarp0) / kPickThreads;
     const uint32_t dyn0 = tc::smem_u32(dyn);
     Ring<C> at;
     int it = 0;
     bool ok = true;
+    // this thread's chunk of 16 bytes in its rows, and its place in a stage: rows
+    // 16 (forward) or 8 (wgrad) apart have the same swizzle
+    constexpr int kCh = C::PASS == kForward ? 8 : 16, kApart = kPickThreads / kCh;
+    constexpr int kRows = (C::PASS == kForward ? C::kBRows : kTileI) / kApart;
+    const int ch = tid % kCh, row0 = tid / kCh;
+    const uint32_t off = (ch >> 3) * 8192 + row0 * 128 + (((ch & 7) ^ (row0 & 7)) << 4);
     for (int tau = blockIdx.x / C::CG; tau < total && ok; tau += gridDim.x / C::CG) {
         const Tile t = tile_at<C>(p, s, tau, MT, rank);
         const int KS = stages_of<C>(p, t), brows = t.npad / C::CG;
-        constexpr int kIdx = (C::kBRows + 31) / 32;
-        int idx[kIdx];  // forward: token rows of B rows lane + 32 i
+        const uint16_t *from[kRows];  // this thread's chunk in each of its rows, NULL: zeros
         if (C::PASS == kForward) {
 #pragma unroll
-            for (int i = 0; i < kIdx; ++i) {
-                const int r = lane + 32 * i;
-                idx[i] = r < brows ? picked_row(p, t.c0 + t.b0 + r, t.c0 + t.n) : -1;
+            for (int i = 0; i < kRows; ++i) {
+                const int r = row0 + kApart * i;
+                const int row = r < brows ? picked_row(p, t.c0 + t.b0 + r, t.c0 + t.n) : -1;
+                from[i] = row >= 0 ? p.rows + int64_t(row) * p.I + 8 * ch : nullptr;
             }
         }
+        const bool picks = C::PASS == kForward || p.sorted_tok;
+        const int m = t.m0 + 8 * ch;
+        int row[kRows];  // wgrad: rows of the next stage this thread fills
+        auto next_rows = [&](int ks) {
+            const int first = t.r0 + kTileI * ks;
+            if (ks < KS && (p.sorted_tok || t.r1 - first < kTileI))
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) row[i] = picked_row(p, first + row0 + kApart * i, t.r1);
+        };
+        if (C::PASS == kWgrad) next_rows((it + group) & 1);
         for (int ks = 0; ks < KS; ++ks, ++it, at.next()) {
-            if (it % kPickWarps != warp) continue;
+            if ((it & 1) != group) continue;
             if (!tc::mbar_wait_warp(&s.empty[at.stage], at.phase ^ 1, kWaitNs)) {
                 ok = false;
                 break;
             }
             const uint32_t a = dyn0 + at.stage * C::kStage, b = a + C::kA;
-            if (C::PASS == kForward) {  // lane: chunk lane % 8 of rows lane / 8 + 4 i
-                const int ch = lane & 7, k = kTileI * ks + 8 * ch;
-                const uint16_t *from = p.rows + k;
+            if (C::PASS == kForward) {
+                const int k = kTileI * ks;
+                const bool kin = k + 8 * ch < p.I;
 #pragma unroll
-                for (int i = 0; i < C::kBRows / 4; ++i) {
-                    const int r = (lane >> 3) + 4 * i;
-                    if (4 * i >= brows) break;
-                    const int row = __shfl_sync(0xffffffffu, idx[i / 8], r & 31);
-                    const bool in = row >= 0 && k < p.I;
-                    if (r < brows)
-                        cp_async16_or_zero(b + r * 128 + ((ch ^ (r & 7)) << 4),
-                                           in ? from + int64_t(row) * p.I : p.rows, in);
+                for (int i = 0; i < kRows; ++i) {
+                    if (kApart * i >= brows) break;
+                    const bool in = kin && from[i];
+                    cp_async16_or_zero(b + off + i * (kApart * 128), in ? from[i] + k : p.rows, in);
                 }
             } else {
                 const int first = t.r0 + kTileI * ks, left = t.r1 - first;
                 const bool tail = left < kTileI;
                 const int rows = tail ? (left + 15) & ~15 : kTileI;
-                const int ch = lane & 15;  // lane: chunk lane % 16 of rows lane / 16 + 2 i
-                const uint32_t off = (ch >> 3) * 8192;
-                if (tail || p.sorted_tok) {
-                    const int m = t.m0 + 8 * ch;
-                    const uint16_t *from = p.rows + m;
-                    int row2[2];
+                if (tail || picks) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) row2[i] = picked_row(p, first + lane + 32 * i, t.r1);
-#pragma unroll
-                    for (int i = 0; i < kTileI / 2; ++i) {
-                        const int r = (lane >> 4) + 2 * i;
-                        if (2 * i >= rows) break;
-                        const int row = __shfl_sync(0xffffffffu, row2[i / 16], r & 31);
-                        const bool in = row >= 0 && m < p.M;
-                        cp_async16_or_zero(a + off + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                                           in ? from + int64_t(row) * p.M : p.rows, in);
+                    for (int i = 0; i < kRows; ++i) {
+                        if (kApart * i >= rows) break;
+                        const bool in = row[i] >= 0 && m < p.M;
+                        cp_async16_or_zero(a + off + i * (kApart * 128), in ? p.rows + int64_t(row[i]) * p.M + m : p.rows,
+                                           in);
                     }
                 }
                 if (tail) {
                     static_assert(C::PASS != kWgrad || C::kBRows == 128, "16 chunks a row");
                     const int n = t.c0 + t.b0 + 8 * ch;
-                    const uint16_t *from = p.dy + int64_t(first) * p.N + n;
-#pragma unroll 8
-                    for (int r = lane >> 4; r < rows; r += 2) {
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) {
+                        const int r = row0 + kApart * i;
+                        if (kApart * i >= rows) break;
                         const bool in = r < left && n < p.N;
-                        cp_async16_or_zero(b + off + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                                           in ? from + int64_t(r) * p.N : p.dy, in);
+                        cp_async16_or_zero(b + off + i * (kApart * 128), in ? p.dy + int64_t(first + r) * p.N + n : p.dy,
+                                           in);
                     }
                 }
+                next_rows(ks + 2);
             }
-            tc::cp_async_wait_all();
+            tc::cp_async_arrive_noinc(&s.landed[at.stage]);
+        }
+    }
+    tc::cp_async_wait_all();
+    if (!ok) stop(s, p.status);
+}
+
+// Relay warp: a stage whose gathered rows have landed is made visible to the
+// tensor cores and counted on rank 0's barrier.
+template <typename C>
+__device__ void relay_stages(const GemmParams &p, GemmSmem &s, int total, int MT, int rank) {
+    const uint32_t full0 = C::CG == 2 ? tc::at_rank(tc::smem_u32(&s.full[0]), 0) : tc::smem_u32(&s.full[0]);
+    Ring<C> at;
+    bool ok = true;
+    for (int tau = blockIdx.x / C::CG; tau < total && ok; tau += gridDim.x / C::CG) {
+        const int KS = stages_of<C>(p, tile_at<C>(p, s, tau, MT, rank));
+        for (int ks = 0; ks < KS; ++ks, at.next()) {
+            if (!tc::mbar_wait_warp(&s.landed[at.stage], at.phase, kWaitNs)) {
+                ok = false;
+                break;
+            }
             tc::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(full0 + at.stage * 8);
+            if (tc::elect_one()) tc::mbar_arrive_cluster(full0 + at.stage * 8);
             __syncwarp();
         }
     }
@@ -594,6 +619,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int i = 0; i < C::kStages; ++i) {
             tc::mbar_init(&s.full[i], 1 + (C::PICK ? C::CG : 0));
             tc::mbar_init(&s.empty[i], 1);
+            tc::mbar_init(&s.landed[i], kPickThreads);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s.tfull[i], 1);
@@ -617,7 +643,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     } else if (warp == kMmaWarp) {
         if (rank == 0) issue_mma<C>(p, s, dyn, total, MT, tmem);
     } else if (warp >= kPickWarp0) {
-        if (C::PICK) gather_tiles<C>(p, s, dyn, total, MT, rank);
+        if constexpr (C::PICK) {
+            if (warp == kRelayWarp) relay_stages<C>(p, s, total, MT, rank);
+            else gather_tiles<C>(p, s, dyn, total, MT, rank);
+        }
     } else if (p.out_fp32) {
         store_tiles<C, float>(p, s, dyn, total, MT, tmem, rank);
     } else if (p.bf16) {
