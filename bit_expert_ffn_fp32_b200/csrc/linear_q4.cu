@@ -2,16 +2,22 @@
 // grouped by expert, w = s*q + m or s*(q-8), for few rows a matrix.
 //
 // Bound by the weights' bytes, so every warp streams codes through its own
-// ring in shared memory (cp.async, kDepth steps of 128 k in flight) and nothing
-// else waits on memory: a warp owns 16 or 32 weight rows and every KS-th step
-// of k, the KS warps of the same rows add their sums in a fixed order at the
-// end. Products run on the tensor cores (mma.m16n8k16, weights as the 16 rows,
-// 8 tokens as the columns): a code q becomes the 16-bit float 16 + q by one
-// shift and one logic operation (q in the top mantissa bits of 16.0), exact in
-// bf16 and fp16, so no weight is rounded and x needs no conversion. The shift
-// comes off a group at a time in fp32:
-//   sum_k w x = s * sum (16 + q) x + (m - 16 s) * sum x      (m = -8 s without min)
-// with sum x from one more mma whose weights are all 1.
+// ring in shared memory (cp.async, kDepth steps of 256 k in flight) and nothing
+// in the loop waits on global memory: a warp owns 16 or 32 weight rows and every
+// KS-th step of k, the KS warps of the same rows add their sums in a fixed order
+// at the end; x is staged once a block, in the order the products read it.
+// Products run on the tensor cores (mma.m16n8k16, weights as the 16 rows, 8
+// tokens as the columns), and what limits them is instructions: 8 codes of a
+// word must take few. A code masked where it stands is the fp16 subnormal
+// q * 2^-24 (bits 0-3 of a half) or q * 2^-20 (bits 4-7), exactly, so a word
+// costs four masks and one shift. x enters as fp16: 128 k of a token are scaled
+// by a power of two that brings their largest to [2^14, 2^15), and the k of the
+// codes at 2^-20 by another 2^-4. bf16 and fp16 values stay exact down to 2^-25
+// of the largest; below that they are rounded at 2^-36 of it, under the 2^-24
+// of the fp32 sums they join. No weight is rounded; in fp32, by group and then
+// by 128 k:
+//   sum_k w x = 2^-e * (s * 2^24 * sum (q 2^-24) (x 2^e) + m * sum x 2^e)   (m = -8 s without min)
+// An infinity or a NaN in x makes its row's results non-finite, all of them.
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,8 +27,8 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kStep = 128;   // k of one ring step: 64 bytes of codes a row
-constexpr int kDepth = 4;    // steps in flight
+constexpr int kStep = 256;   // k of one ring step: 128 bytes of codes a row
+constexpr int kDepth = 2;    // steps in flight
 
 struct Q4Params {
     const uint8_t *codes;
@@ -36,79 +42,73 @@ struct Q4Params {
     void *out;
     int out_fp32, swiglu;
     int ks_log2;             // warps that share the same rows, log2
+    int ts_log2;             // tokens a tile of staged x holds, log2 (3 unless a single tile is never full)
+    int chunk;               // steps of x staged at a time, a multiple of kDepth << ks_log2
     int scales_in_words;     // a step's scales of a row can be read as one aligned word
     int32_t *status;
 };
 
-template <typename X>
-struct Codes16;  // 16 + q as X, two at a time: nibbles j and j + 4 of a code word
-template <>
-struct Codes16<__nv_bfloat16> {
-    template <int J>
-    static __device__ __forceinline__ uint32_t at(uint32_t w) {
-        constexpr int sh = 4 * J - 3;  // nibble j to bits 3..6
-        return ((sh < 0 ? w << (sh < 0 ? -sh : 0) : w >> (sh < 0 ? 0 : sh)) & 0x00780078u) | 0x41804180u;
-    }
-    static constexpr uint32_t kOnes = 0x3F803F80u;
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-template <>
-struct Codes16<__half> {
-    template <int J>
-    static __device__ __forceinline__ uint32_t at(uint32_t w) {
-        constexpr int sh = 4 * J - 6;  // nibble j to bits 6..9
-        return ((sh < 0 ? w << (sh < 0 ? -sh : 0) : w >> (sh < 0 ? 0 : sh)) & 0x03C003C0u) | 0x4C004C00u;
-    }
-    static constexpr uint32_t kOnes = 0x3C003C00u;
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-
-// Bytes from one weight row to the next in a ring step: 64 of codes, padded so
-// that the fragment reads (4, 8 or 16 bytes a lane) fall into different banks.
-template <int G>
-constexpr int kRowStride = G == 32 ? 80 : G == 64 ? 96 : 64;
-
-template <int G, int RG>
-constexpr int ring_bytes() { return kDepth * 16 * RG * kRowStride<G>; }
-constexpr int kPartStride = 36;  // floats from one token's 32 partial sums to the next
-template <int G, int RG, int NB>
-constexpr int warp_smem() {
-    return ring_bytes<G, RG>() > NB * 8 * kPartStride * 4 ? ring_bytes<G, RG>() : NB * 8 * kPartStride * 4;
+// The four half pairs of a code word as fp16: codes (0, 4) and (2, 6) times
+// 2^-24, codes (1, 5) and (3, 7) times 2^-20.
+__device__ __forceinline__ void halves_of(uint32_t w, uint32_t (&h)[4]) {
+    const uint32_t v = w >> 8;
+    h[0] = w & 0x000F000Fu;
+    h[1] = w & 0x00F000F0u;
+    h[2] = v & 0x000F000Fu;
+    h[3] = v & 0x00F000F0u;
 }
+__device__ __forceinline__ void mma_fp16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A ring step holds 128 bytes of codes a row, 16-byte chunks swizzled so that
+// the fragment reads (4, 8 or 16 bytes a lane) fall into different banks.
+template <int G>
+__device__ __forceinline__ int swizzle(int row) {
+    return G == 32 ? row & 7 : G == 64 ? (row & 3) * 2 : (row & 1) * 4;
+}
+constexpr int kPartStride = 36;  // floats from one token's 32 partial sums to the next
+// Per warp: the ring, later the partial sums; then the step's scale pairs.
+template <int RG, int NB>
+constexpr int kRingBytes = kDepth * 16 * RG * 128 > NB * 8 * kPartStride * 4 ? kDepth * 16 * RG * 128
+                                                                           : NB * 8 * kPartStride * 4;
+template <int G, int RG, int NB>
+constexpr int kWarpBytes = kRingBytes<RG, NB> + (kStep / G) * 16 * RG * 8;
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
-// The scales (or mins) of one row in one step, 128 / G of them, low first.
-template <int G>
-__device__ __forceinline__ uint2 load_scales(const __half *row, int first, int count, bool words) {
-    uint2 v = make_uint2(0, 0);
-    const __half *p = row + first;
-    if (words) {
-        if (G == 32) v = __ldg(reinterpret_cast<const uint2 *>(p));
-        else if (G == 64) v.x = __ldg(reinterpret_cast<const uint32_t *>(p));
-        else v.x = __ldg(reinterpret_cast<const unsigned short *>(p));
-        return v;
-    }
-    const unsigned short *h = reinterpret_cast<const unsigned short *>(p);
-    if (first < count) v.x = __ldg(h);
-    if (G <= 64 && first + 1 < count) v.x |= uint32_t(__ldg(h + 1)) << 16;
-    if (G == 32 && first + 2 < count) v.y = __ldg(h + 2);
-    if (G == 32 && first + 3 < count) v.y |= uint32_t(__ldg(h + 3)) << 16;
-    return v;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ float half_at(uint2 v, int j) {
-    const uint32_t w = j < 2 ? v.x : v.y;
+// The scales (or mins) of one row in one step, 256 / G of them, low first.
+template <int G>
+__device__ __forceinline__ uint4 load_scales(const __half *row, int first, int count, bool words) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const __half *p = row + first;
+    if (words) {
+        if constexpr (G == 32) v = __ldg(reinterpret_cast<const uint4 *>(p));
+        if constexpr (G == 64) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            v.x = u.x, v.y = u.y;
+        }
+        if constexpr (G == 128) v.x = __ldg(reinterpret_cast<const uint32_t *>(p));
+        return v;
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < kStep / G; ++j)
+        if (first + j < count) w[j / 2] |= uint32_t(__ldg(reinterpret_cast<const unsigned short *>(p) + j)) << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float half_at(const uint4 &v, int j) {
+    const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
     return __half2float(__ushort_as_half(static_cast<unsigned short>(j & 1 ? w >> 16 : w & 0xFFFF)));
 }
 
@@ -116,9 +116,9 @@ __device__ __forceinline__ float half_at(uint2 v, int j) {
 // groups a warp owns (2: 32 rows, or with SwiGLU 16 gate rows and their 16 up
 // rows); NB: tiles of 8 tokens whose sums a warp keeps.
 template <typename X, int G, int RG, int NB>
-__global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 3 : 2) q4_kernel(const __grid_constant__ Q4Params p) {
-    constexpr int R = 16 * RG, RS = kRowStride<G>, W = G / 32, J = kStep / G;
-    extern __shared__ __align__(16) unsigned char smem[];
+__global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const __grid_constant__ Q4Params p) {
+    constexpr int R = 16 * RG, W = G / 32, J = kStep / G;
+    extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int KS = 1 << p.ks_log2, ks = warp & (KS - 1);
     const int units = (p.swiglu ? p.N / 2 : p.N) / (p.swiglu ? 16 : R);
@@ -126,11 +126,10 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 3 : 2) q4_kernel(const 
 
     int slot = p.slot, r0 = 0, r1 = p.T;
     if (p.slot_of) {
-        const int na = p.active[0];
+        const int na = p.active[0], e = p.active[1 + blockIdx.y];  // E + 1 entries: blockIdx.y < E
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (na < 0 || na > p.E))
             flag(p.status, MOE_DEV_BAD_INDEX);
         if (int(blockIdx.y) >= na) return;
-        const int e = p.active[1 + blockIdx.y];
         if (e < 0 || e >= p.E) {
             if (threadIdx.x == 0) flag(p.status, MOE_DEV_BAD_INDEX);
             return;
@@ -154,12 +153,22 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 3 : 2) q4_kernel(const 
     const bool busy = unit < units;
     const int steps = (p.K + kStep - 1) / kStep, groups = p.K / G;
     const int64_t slot_row = int64_t(slot) * p.N;
-    const uint32_t ring = tc::smem_u32(smem) + warp * warp_smem<G, RG, NB>();
-    const unsigned char *ring_ptr = smem + warp * warp_smem<G, RG, NB>();
-    // this lane's 16-byte parts of a step: part t of rows g + 8i
-    const uint8_t *src = p.codes + (slot_row + (busy ? weight_row(g) : 0)) * (p.K / 2) + 16 * t;
-    const int64_t up8 = int64_t(8) * (p.K / 2), up16 = p.swiglu ? int64_t(p.N / 2) * (p.K / 2) : 2 * up8;
-    const uint32_t dst = ring + g * RS + 16 * t;
+    unsigned char *mine = smem + warp * kWarpBytes<G, RG, NB>;
+    const uint32_t ring = tc::smem_u32(mine);
+    float4 *pairs = reinterpret_cast<float4 *>(mine + kRingBytes<RG, NB>);  // [J][RG][8]: {s, c} of rows g and g + 8
+    // x of a chunk of k, 16 bytes (8 k) of one token each: [tile][step][32 units][tokens], a step's units in the order
+    // (group, code word of a lane, lane t); then the sums of the scaled x:
+    // [tile][group][8 tokens]
+    const int tile_units = p.chunk * (kStep / 8) << p.ts_log2;
+    uint4 *xs = reinterpret_cast<uint4 *>(smem + kWarps * kWarpBytes<G, RG, NB>);
+    float *xsum = reinterpret_cast<float *>(xs + NB * tile_units);
+    float *xdown = xsum + NB * p.chunk * J * 8;  // 2^-e: [tile][128 k][8 tokens]
+    // this lane's 16-byte parts of a step: parts t and t + 4 of rows g + 8i
+    const uint8_t *src[2 * RG];
+#pragma unroll
+    for (int i = 0; i < 2 * RG; ++i)
+        src[i] = p.codes + (slot_row + (busy ? weight_row(g + 8 * i) : 0)) * (p.K / 2) + 16 * t;
+    const uint32_t dst = ring + g * 128 + ((t ^ swizzle<G>(g)) << 4);  // rows 8 apart have the same swizzle
     const __half *srow = nullptr, *mrow = nullptr;  // scales of row `lane`
     {
         const int64_t row = slot_row + (busy ? weight_row(lane & (R - 1)) : 0);
@@ -168,46 +177,43 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 3 : 2) q4_kernel(const 
     }
     auto issue = [&](int step, int stage) {
         if (busy && step < steps) {
-            const bool in = step * kStep + 32 * t < p.K;
-            const uint8_t *s = src + int64_t(step) * (kStep / 2);
-            const uint32_t d = dst + stage * (R * RS);
+            const uint32_t d = dst + stage * (R * 128);
+            const int64_t at = int64_t(step) * (kStep / 2);
+            const int left = p.K - step * kStep;
+            if (left >= kStep) {
 #pragma unroll
-            for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint8_t *from = s + (rg ? up16 : 0) + (i ? up8 : 0);
-                    cp_async16_or_zero(d + (16 * rg + 8 * i) * RS, in ? from : p.codes, in);
+                for (int i = 0; i < 2 * RG; ++i) {
+                    cp_async16(d + i * 1024, src[i] + at);
+                    cp_async16((d + i * 1024) ^ 64, src[i] + at + 64);
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * RG; ++i) {
+                    cp_async16_or_zero(d + i * 1024, 32 * t < left ? src[i] + at : p.codes, 32 * t < left);
+                    cp_async16_or_zero((d + i * 1024) ^ 64, 128 + 32 * t < left ? src[i] + at + 64 : p.codes,
+                                       128 + 32 * t < left);
+                }
+            }
         }
         tc::cp_async_commit();
     };
-    uint2 sc[kDepth], mn[kDepth];
-    auto issue_scales = [&](int step, uint2 &s, uint2 &m) {
+    uint4 sc[kDepth], mn[kDepth];
+    auto issue_scales = [&](int step, uint4 &s, uint4 &m) {
         if (busy && step < steps) {
             s = load_scales<G>(srow, step * J, groups, p.scales_in_words);
             if (mrow) m = load_scales<G>(mrow, step * J, groups, p.scales_in_words);
         }
     };
 
-    const uint32_t ones[4] = {Codes16<X>::kOnes, Codes16<X>::kOnes, Codes16<X>::kOnes, Codes16<X>::kOnes};
-    for (int pass = r0; pass < r1; pass += 8 * NB) {
-        const int n = min(8 * NB, r1 - pass);
-        // columns (tokens) of this lane's B fragments: token 8 nb + g
-        const X *xrow[NB];
+    const int per_pass = NB == 1 ? 1 << p.ts_log2 : 8 * NB;
+    for (int pass = r0; pass < r1; pass += per_pass) {
+        const int n = min(per_pass, r1 - pass), tiles = (n + 7) / 8;
+        const int ts = n > 4 ? 3 : n > 2 ? 2 : n > 1 ? 1 : 0, TS = 1 << ts;  // tokens a tile of x holds here
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            xrow[nb] = nullptr;
-            if (8 * nb + g < n) {
-                int row = pass + 8 * nb + g;
-                if (p.sorted_tok) {
-                    row = p.sorted_tok[row];
-                    if (row < 0 || row >= p.T) {
-                        if (blockIdx.x == 0 && warp == 0 && t == 0) flag(p.status, MOE_DEV_BAD_INDEX);
-                        row = -1;
-                    }
-                }
-                if (row >= 0) xrow[nb] = static_cast<const X *>(p.x) + int64_t(row) * p.K + (G / 4) * t;
-            }
+        for (int d = 0; d < kDepth; ++d) {
+            sc[d] = mn[d] = make_uint4(0, 0, 0, 0);
+            issue(ks + d * KS, d);
+            issue_scales(ks + d * KS, sc[d], mn[d]);
         }
         float sum[NB][RG][4];
 #pragma unroll
@@ -216,107 +222,205 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 3 : 2) q4_kernel(const 
             for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[nb][rg][i] = 0.f;
+        for (int c0 = 0; c0 < steps; c0 += p.chunk) {
+        // stage x: a code word's halves hold codes j and j + 4, so k j and k j + 4 share a register of x; those of
+        // odd j scaled down by the 2^4 that their codes are high
+        const int quads = min(p.chunk * (kStep / 32), p.K / 32 - c0 * (kStep / 32)), cgroups = quads * 32 / G;  // of 32 k
+        const int quads4 = (quads + 3) & ~3;  // of whole 128 k, so that the four of one stay together
+        if (c0) __syncthreads();
+        for (int i = threadIdx.x; i < ((tiles * quads4 << ts) + 31 & ~31); i += 32 * kWarps) {
+            // one token's 32 k: lanes of one token are TS apart, so a group's sum is a shuffle away
+            const int tq = i >> ts, nb = tq / quads4, quad = tq - nb * quads4, tok = 8 * nb + (i & (TS - 1));
+            int row = -1;
+            if (nb < tiles && quad < quads && tok < n) {
+                row = pass + tok;
+                if (p.sorted_tok) {
+                    row = p.sorted_tok[row];
+                    if (row < 0 || row >= p.T) {
+                        if (blockIdx.x == 0 && quad == 0) flag(p.status, MOE_DEV_BAD_INDEX);
+                        row = -1;
+                    }
+                }
+            }
+            uint4 v[4];
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            sc[d] = mn[d] = make_uint2(0, 0);
-            issue(ks + d * KS, d);
-            issue_scales(ks + d * KS, sc[d], mn[d]);
+            for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
+            if (row >= 0) {
+                const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const X *>(p.x) + int64_t(row) * p.K) +
+                                    (c0 * (kStep / 32) + quad) * 4;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = __ldg(from + k);
+            }
+            // the power of two of these 128 k: 14 less the exponent of their largest
+            float x[4][8], most = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const X *h = reinterpret_cast<const X *>(&v[k]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[k][j] = to_f32(h[j]);
+                    most = fmaxf(most, fabsf(x[k][j]));
+                }
+            }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, TS));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2 * TS));
+            const int e = min(14 - (int(__float_as_uint(most) >> 23) - 127), 100);
+            const float up = __uint_as_float(uint32_t(127 + e) << 23);
+            float part = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float eight = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[k][j] *= up;
+                    eight += x[k][j];
+                }
+                part += eight;
+            }
+            if (G >= 64) part += __shfl_xor_sync(0xffffffffu, part, TS);
+            if (G >= 128) part += __shfl_xor_sync(0xffffffffu, part, 2 * TS);
+            if (nb < tiles && quad < quads) {
+                const int slot8 = i & (TS - 1);
+                if ((quad & (G / 32 - 1)) == 0) xsum[(nb * cgroups + quad / (G / 32)) * 8 + slot8] = part;
+                if ((quad & 3) == 0)
+                    xdown[(nb * p.chunk * 2 + quad / 4) * 8 + slot8] = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int unit8 = quad * 4 + k, q = unit8 & (G / 8 - 1);
+                    const int at = (unit8 & ~(G / 8 - 1)) + (q % W) * 4 + q / W;
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float f = j & 1 ? 0.0625f : 1.f;
+                        const __half2 two = __floats2half2_rn(x[k][j] * f, x[k][j + 4] * f);
+                        h[j] = *reinterpret_cast<const uint32_t *>(&two);
+                    }
+                    xs[nb * tile_units + (at << ts) + slot8] = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            }
         }
-        for (int step0 = ks; step0 < steps; step0 += kDepth * KS) {
+        __syncthreads();
+        for (int step0 = c0 + ks; step0 < min(steps, c0 + p.chunk); step0 += kDepth * KS) {
 #pragma unroll
             for (int d = 0; d < kDepth; ++d) {
                 const int step = step0 + d * KS;
                 if (step < steps && busy) {
                     tc::cp_async_wait<kDepth - 1>();
-                    __syncwarp();
-                    const unsigned char *st = ring_ptr + d * (R * RS) + g * RS + (G / 8) * t;
+                    if (RG == 2 || lane < 16) {  // scale pairs of this lane's row
+                        float2 *own = reinterpret_cast<float2 *>(pairs) + (lane >> 4) * 16 + 2 * (lane & 7) +
+                                      ((lane >> 3) & 1);
 #pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        if (step * J + j >= groups) break;
+                        for (int j = 0; j < J; ++j) {
+                            const float s = half_at(sc[d], j);
+                            own[j * R] = make_float2(s * 16777216.f, p.min ? half_at(mn[d], j) : -8.f * s);
+                        }
+                    }
+                    __syncwarp();
+                    const unsigned char *st = mine + d * (R * 128) + g * 128;
+                    const uint4 *xstep = xs + (((step - c0) * (kStep / 8) + t) << ts) + (g & (TS - 1));
+                    // adds group j to y, in the scale of its 128 k
+                    auto group = [&](int j, float(&y)[NB][RG][4]) {
                         uint32_t w[RG][2][W];
 #pragma unroll
                         for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const unsigned char *from = st + (16 * rg + 8 * i) * RS + j * (G / 2);
-                                if (W == 1) w[rg][i][0] = *reinterpret_cast<const uint32_t *>(from);
-                                if (W == 2) {
+                                // bytes (G / 8) t of the group's G / 2, in swizzled 16-byte chunks
+                                const int byte = j * (G / 2) + (G / 8) * t;
+                                const unsigned char *from = st + (16 * rg + 8 * i) * 128 +
+                                                            (((byte >> 4) ^ swizzle<G>(g)) << 4) + (byte & 15);
+                                if constexpr (W == 1) {
+                                    w[rg][i][0] = *reinterpret_cast<const uint32_t *>(from);
+                                } else if constexpr (W == 2) {
                                     const uint2 v = *reinterpret_cast<const uint2 *>(from);
-                                    w[rg][i][0] = v.x;
-                                    w[rg][i][W - 1] = v.y;
-                                }
-                                if (W == 4) {
+                                    w[rg][i][0] = v.x, w[rg][i][1] = v.y;
+                                } else {
                                     const uint4 v = *reinterpret_cast<const uint4 *>(from);
-                                    w[rg][i][0] = v.x;
-                                    w[rg][i][W > 1 ? 1 : 0] = v.y;
-                                    w[rg][i][W > 2 ? 2 : 0] = v.z;
-                                    w[rg][i][W - 1] = v.w;
+                                    w[rg][i][0] = v.x, w[rg][i][1] = v.y, w[rg][i][2] = v.z, w[rg][i][3] = v.w;
                                 }
                             }
-                        float acc[NB][RG + 1][4];
+                        float acc[NB][RG][4];
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                            for (int rg = 0; rg <= RG; ++rg)
+                            for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) acc[nb][rg][i] = 0.f;
 #pragma unroll
                         for (int wi = 0; wi < W; ++wi) {
-                            uint32_t a[RG][2][4];
+                            uint32_t lo[RG][4], hi[RG][4];
 #pragma unroll
                             for (int rg = 0; rg < RG; ++rg) {
-                                const uint32_t lo = w[rg][0][wi], hi = w[rg][1][wi];
-                                a[rg][0][0] = Codes16<X>::template at<0>(lo);
-                                a[rg][0][1] = Codes16<X>::template at<0>(hi);
-                                a[rg][0][2] = Codes16<X>::template at<1>(lo);
-                                a[rg][0][3] = Codes16<X>::template at<1>(hi);
-                                a[rg][1][0] = Codes16<X>::template at<2>(lo);
-                                a[rg][1][1] = Codes16<X>::template at<2>(hi);
-                                a[rg][1][2] = Codes16<X>::template at<3>(lo);
-                                a[rg][1][3] = Codes16<X>::template at<3>(hi);
+                                halves_of(w[rg][0][wi], lo[rg]);
+                                halves_of(w[rg][1][wi], hi[rg]);
                             }
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb) {
-                                if (NB > 1 && 8 * nb >= n) break;
-                                uint4 xv = make_uint4(0, 0, 0, 0);  // 8 consecutive k of token g
-                                if (xrow[nb])
-                                    xv = __ldg(reinterpret_cast<const uint4 *>(xrow[nb] + step * kStep + j * G +
-                                                                               8 * wi));
-                                // nibbles j and j + 4 share a register of a, so k j and k j + 4 one of b
-                                const uint32_t b00 = __byte_perm(xv.x, xv.z, 0x5410),
-                                               b01 = __byte_perm(xv.x, xv.z, 0x7632),
-                                               b10 = __byte_perm(xv.y, xv.w, 0x5410),
-                                               b11 = __byte_perm(xv.y, xv.w, 0x7632);
+                                if (NB > 1 && nb >= tiles) break;
+                                const uint4 xv = xstep[nb * tile_units + ((j * W + wi) * 4 << ts)];
 #pragma unroll
                                 for (int rg = 0; rg < RG; ++rg) {
-                                    Codes16<X>::mma(acc[nb][rg], a[rg][0], b00, b01);
-                                    Codes16<X>::mma(acc[nb][rg], a[rg][1], b10, b11);
+                                    mma_fp16(acc[nb][rg], lo[rg][0], hi[rg][0], lo[rg][1], hi[rg][1], xv.x, xv.y);
+                                    mma_fp16(acc[nb][rg], lo[rg][2], hi[rg][2], lo[rg][3], hi[rg][3], xv.z, xv.w);
                                 }
-                                Codes16<X>::mma(acc[nb][RG], ones, b00, b01);
-                                Codes16<X>::mma(acc[nb][RG], ones, b10, b11);
                             }
                         }
-                        // scale of this lane's row, then those of the rows this lane has sums of
-                        const float s_own = half_at(sc[d], j);
-                        const float c_own = p.min ? fmaf(-16.f, s_own, half_at(mn[d], j)) : -24.f * s_own;
+                        float2 x01[NB];
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            if (NB == 1 || nb < tiles)
+                                x01[nb] = *reinterpret_cast<const float2 *>(
+                                    xsum + (nb * cgroups + (step - c0) * J + j) * 8 + 2 * t);
 #pragma unroll
                         for (int rg = 0; rg < RG; ++rg) {
-                            const float s_lo = __shfl_sync(0xffffffffu, s_own, 16 * rg + g);
-                            const float s_hi = __shfl_sync(0xffffffffu, s_own, 16 * rg + 8 + g);
-                            const float c_lo = __shfl_sync(0xffffffffu, c_own, 16 * rg + g);
-                            const float c_hi = __shfl_sync(0xffffffffu, c_own, 16 * rg + 8 + g);
+                            const float4 f = pairs[(j * RG + rg) * 8 + g];  // s 2^24, m of row g, then of row g + 8
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb) {
-                                if (NB > 1 && 8 * nb >= n) break;
-                                float(&y)[4] = sum[nb][rg];
+                                if (NB > 1 && nb >= tiles) break;
+                                float(&o)[4] = y[nb][rg];
                                 const float(&v)[4] = acc[nb][rg];
-                                const float x0 = acc[nb][RG][0], x1 = acc[nb][RG][1];
-                                y[0] = fmaf(s_lo, v[0], fmaf(c_lo, x0, y[0]));
-                                y[1] = fmaf(s_lo, v[1], fmaf(c_lo, x1, y[1]));
-                                y[2] = fmaf(s_hi, v[2], fmaf(c_hi, x0, y[2]));
-                                y[3] = fmaf(s_hi, v[3], fmaf(c_hi, x1, y[3]));
+                                o[0] = fmaf(f.x, v[0], fmaf(f.y, x01[nb].x, o[0]));
+                                o[1] = fmaf(f.x, v[1], fmaf(f.y, x01[nb].y, o[1]));
+                                o[2] = fmaf(f.z, v[2], fmaf(f.w, x01[nb].x, o[2]));
+                                o[3] = fmaf(f.z, v[3], fmaf(f.w, x01[nb].y, o[3]));
                             }
                         }
+                    };
+                    // `count` groups of 128 k, then out of their scale
+                    auto half_step = [&](int h, int count, bool whole) {
+                        float y[NB][RG][4];
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) y[nb][rg][i] = 0.f;
+                        if (whole) {
+#pragma unroll
+                            for (int j = 0; j < J / 2; ++j) group(h * (J / 2) + j, y);
+                        } else {
+#pragma unroll 1
+                            for (int j = 0; j < count; ++j) group(h * (J / 2) + j, y);
+                        }
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            if (NB > 1 && nb >= tiles) break;
+                            const float2 down = *reinterpret_cast<const float2 *>(
+                                xdown + ((nb * p.chunk + step - c0) * 2 + h) * 8 + 2 * t);
+#pragma unroll
+                            for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    sum[nb][rg][i] = fmaf(i & 1 ? down.y : down.x, y[nb][rg][i], sum[nb][rg][i]);
+                        }
+                    };
+                    const int here = groups - step * J;
+                    if (here >= J) {  // in one piece, so that the groups' products overlap
+                        half_step(0, J / 2, true);
+                        half_step(1, J / 2, true);
+                    } else {
+                        half_step(0, min(here, J / 2), false);
+                        if (here > J / 2) half_step(1, here - J / 2, false);
                     }
                     __syncwarp();  // every lane has read the stage before it is refilled
                     issue(step + kDepth * KS, d);
@@ -324,10 +428,11 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 3 : 2) q4_kernel(const 
                 }
             }
         }
+        }
         tc::cp_async_wait<0>();
         __syncthreads();  // the rings are free: partial sums [token][row] take their place
         if (busy) {
-            float *part = reinterpret_cast<float *>(smem + warp * warp_smem<G, RG, NB>());
+            float *part = reinterpret_cast<float *>(mine);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -343,9 +448,9 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 3 : 2) q4_kernel(const 
         const int cols = p.swiglu ? p.N / 2 : p.N;
         for (int i = threadIdx.x; i < n * in_block; i += 32 * kWarps) {
             const int tok = i / in_block, c = i - tok * in_block, u = c / per_unit, row = c - u * per_unit;
-            const unsigned char *from = smem + (u << p.ks_log2) * warp_smem<G, RG, NB>();
+            const unsigned char *from = smem + (u << p.ks_log2) * kWarpBytes<G, RG, NB>;
             float y = 0.f, up = 0.f;
-            for (int k = 0; k < KS; ++k, from += warp_smem<G, RG, NB>()) {
+            for (int k = 0; k < KS; ++k, from += kWarpBytes<G, RG, NB>) {
                 const float *part = reinterpret_cast<const float *>(from) + tok * kPartStride;
                 y += part[row];
                 if (RG == 2 && p.swiglu) up += part[16 + row];
@@ -361,11 +466,15 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 3 : 2) q4_kernel(const 
 
 template <typename X, int G, int RG, int NB>
 moe_status launch(Q4Params &p, int experts, cudaStream_t stream) {
-    constexpr int smem = kWarps * warp_smem<G, RG, NB>();
-    static_assert(smem <= 100 * 1024, "two blocks of an SM do not fit");
+    // x of the whole of k where two blocks of an SM still fit (one, with more
+    // tiles of tokens), else in chunks
+    const int steps = (p.K + kStep - 1) / kStep, unit = kDepth << p.ks_log2, per_step = NB * (kStep * 2 << p.ts_log2);
+    const int whole = (steps + unit - 1) / unit, fit = (NB == 1 ? 36 : 128) * 1024 / (per_step * unit);
+    p.chunk = std::max(1, std::min(whole, fit)) * unit;
+    const size_t smem = size_t(kWarps) * kWarpBytes<G, RG, NB> + size_t(p.chunk) * (per_step + NB * (kStep / G) * 32 + NB * 64);
     // set on every call: the attribute belongs to the current device's context
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(q4_kernel<X, G, RG, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 smem) != cudaSuccess) {
+    if (smem > 232448 || cudaFuncSetAttribute(q4_kernel<X, G, RG, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              int(smem)) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
@@ -402,20 +511,27 @@ moe_status run_q4(const moe_q4weights *W, Q4Params &p, const void *x, int dtype,
     p.out = out;
     p.out_fp32 = out_dtype == MOE_FP32;
     p.swiglu = act == MOE_ACT_SWIGLU;
-    p.scales_in_words = W->K % kStep == 0 && reinterpret_cast<uintptr_t>(W->scale) % 8 == 0 &&
-                        reinterpret_cast<uintptr_t>(W->min) % 8 == 0;
-    // Enough warps to keep every SM's memory pipe full (16 each): split k over
-    // up to the 8 warps of a block, then halve the rows a warp owns.
-    constexpr int64_t kWant = 148 * 16;
-    const int steps = (p.K + kStep - 1) / kStep;
-    int rg = 2, ks = 0;
-    const int64_t warps = int64_t(p.N / 32) * experts;
-    while (ks < 3 && (warps << ks) < kWant && (2 << ks) <= steps) ++ks;
-    if (!p.swiglu && (warps << ks) < kWant) rg = 1;
-    p.ks_log2 = ks;
+    p.scales_in_words = W->K % kStep == 0 && reinterpret_cast<uintptr_t>(W->scale) % 16 == 0 &&
+                        reinterpret_cast<uintptr_t>(W->min) % 16 == 0;
     // Token tiles: as many as the rows a matrix has on average (at most T) fill.
     const int rows = std::min(p.T, 2 * ((p.P + experts - 1) / experts));
     const int nb = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    p.ts_log2 = nb > 1 || p.T > 4 ? 3 : p.T > 2 ? 2 : p.T > 1 ? 1 : 0;
+    // Warps that share rows: as many as leave all blocks running at once (two an
+    // SM), up to 8 (4 with four token tiles, whose x would not fit); then 16 rows
+    // a warp. Where the blocks take several turns anyway, pairs of warps, unless
+    // k is too short to split. Measured (warps a row: us): gate and up rows of
+    // one token 1: 13.0, 2: 8.8, 4: 8.2, 8: 10.7 (480 blocks); 8192 x 8192, one
+    // token 1: 32, 2: 19, 4: 12.8, 8: 12.1; gate and up rows of 37 tokens 1: 91,
+    // 2: 79, 4: 89; down rows (3 steps of k) of four tokens 1: 17, 2: 20, 4: 24.
+    constexpr int64_t kSlots = 148 * 2 * kWarps;
+    const int steps = (p.K + kStep - 1) / kStep, most = nb == 4 ? 2 : 3;
+    int rg = 2, ks = 0;
+    const int64_t units = int64_t(p.N / 32) * experts;
+    while (ks < most && (units << (ks + 1)) <= kSlots && (2 << ks) <= steps) ++ks;
+    if (!p.swiglu && (units << (ks + 1)) <= kSlots) rg = 1;
+    if (units > kSlots && steps >= 8) ks = 1;
+    p.ks_log2 = ks;
     return dtype == MOE_BF16 ? launch_x<__nv_bfloat16>(p, W->group, rg, nb, experts, stream)
                              : launch_x<__half>(p, W->group, rg, nb, experts, stream);
 }

@@ -135,9 +135,12 @@ def ptr(t) -> int | None:
 
 
 def stream_handle(stream=None) -> int | None:
+    """cudaStream_t of a torch stream, by default the current GPU's current one."""
+    if stream is not None:
+        return stream.cuda_stream or None
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream or None
+    # the handle alone: torch.cuda.current_stream() builds a Stream around it (3.4 us a call against 0.3)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
 
 
 def qmatrix(codes, scale, mn=None, hi=None) -> QMatrix:
@@ -353,47 +356,58 @@ def debug_wait_probe(counter, target: int, elapsed_ns, dev_status, stream=None) 
 
 
 # ------------------------------------------------------------------ 4-bit and unquantised products, gradients
-def _codes_of_dtypes() -> dict:
-    import torch
-    # int16 tensors hold bf16 bits, as for the layer's x
-    return {torch.bfloat16: BF16, torch.int16: BF16, torch.float16: FP16, torch.float32: FP32}
+class _Types:
+    """torch's types and their moe_dtype codes, once torch is loaded."""
+    code: dict = {}
+    int32 = device = None
 
-
-_DTYPES: dict = {}
+    @classmethod
+    def load(cls) -> None:
+        import torch
+        # int16 tensors hold bf16 bits, as for the layer's x
+        cls.code = {torch.bfloat16: BF16, torch.int16: BF16, torch.float16: FP16, torch.float32: FP32}
+        cls.int32 = torch.int32
+        cls.device = torch.cuda.current_device
 
 
 def dtype_code(t) -> int:
     """moe_dtype of a tensor (int16 = bf16 bits)."""
-    if not _DTYPES:
-        _DTYPES.update(_codes_of_dtypes())
-    code = _DTYPES.get(t.dtype)
+    if not _Types.code:
+        _Types.load()
+    code = _Types.code.get(t.dtype)
     if code is None:
         raise ValueError(f"no moe_dtype for {t.dtype}: bfloat16 (or int16 bits), float16 and float32 are known")
     return code
 
 
-def _same_place(*sized) -> int:
-    """Check (tensor, elements) pairs before their addresses go to the library:
-    contiguous tensors of one GPU, the current one, of at least so many
-    elements. Returns the GPU's index."""
-    dev = sized[0][0].get_device()
-    for t, n in sized:
-        if t is not None and not (t.numel() >= n and t.is_contiguous() and t.get_device() == dev):
-            raise ValueError(f"a contiguous tensor of {n} or more elements on GPU {dev} is wanted, got "
-                             f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-    import torch
+def _address(t, n: int, dev: int) -> int:
+    """Address of a tensor, looked at before it goes to the library: contiguous,
+    on GPU `dev`, of n elements at least."""
+    if t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"a contiguous tensor of {n} or more elements on GPU {dev} is wanted, got {tuple(t.shape)}, "
+                         f"strides {t.stride()}, on {t.device}")
+    return t.data_ptr()
+
+
+def _table(t, n: int, dev: int) -> int | None:
+    """_address of an int32 table, None for None."""
+    if t is None:
+        return None
+    if t.dtype != _Types.int32:
+        raise ValueError(f"an int32 tensor is wanted, got {t.dtype}")
+    return _address(t, n, dev)
+
+
+def _place_of(t) -> int:
+    """The GPU of a tensor, which has to be the current one: the library launches there."""
+    if _Types.device is None:
+        _Types.load()
+    dev = t.get_device()
     if dev < 0:
         raise ValueError("GPU tensors are wanted")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on GPU {dev}, the current GPU is {torch.cuda.current_device()}")
+    if dev != _Types.device():
+        raise ValueError(f"the tensors are on GPU {dev}, the current GPU is {_Types.device()}")
     return dev
-
-
-def _int32(*tensors) -> None:
-    import torch
-    for t in tensors:
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError(f"an int32 tensor is wanted, got {t.dtype}")
 
 
 def q4_weights(codes, scale, min, group: int) -> Q4Weights:
@@ -420,84 +434,90 @@ def q4_weights(codes, scale, min, group: int) -> Q4Weights:
 
 def linear_q4(W: Q4Weights, slot: int, x, T: int, out, act: int = ACT_NONE, stream=None) -> None:
     """out[t] = W[slot] x[t]; out [T][N] (SwiGLU: [T][N/2]) in x's type or fp32."""
-    _same_place((W.tensors[0], 0), (x, T * W.K), (out, T * W.N // (1 + act)))
-    check("moe_linear_q4", lib.moe_linear_q4(C.addressof(W), slot, ptr(x), dtype_code(x), T, act, ptr(out),
-                                             dtype_code(out), stream_handle(stream)))
+    dev = _place_of(W.tensors[0])
+    code = lib.moe_linear_q4(C.addressof(W), slot, _address(x, T * W.K, dev), dtype_code(x), T, act,
+                             _address(out, T * W.N // (1 + (act == ACT_SWIGLU)), dev), dtype_code(out),
+                             stream_handle(stream))
+    if code:
+        raise MoeError("moe_linear_q4", code)
 
 
 def expert_linear_q4(W: Q4Weights, slot_of, x, T: int, E: int, k: int, offsets, sorted_tok, active, out,
                      act: int = ACT_NONE, dev_status=None, stream=None) -> None:
     """out[s] = W[slot_of[e]] x_s for the sorted pairs s of every active expert e
     (x_s = x[sorted_tok[s]], or x[s] with sorted_tok None)."""
-    P = T * k
-    _same_place((W.tensors[0], 0), (slot_of, E), (x, (P if sorted_tok is None else T) * W.K), (offsets, E + 1),
-                (sorted_tok, P), (active, E + 1), (out, P * W.N // (1 + act)), (dev_status, 1))
-    _int32(slot_of, offsets, sorted_tok, active, dev_status)
-    check("moe_expert_linear_q4",
-          lib.moe_expert_linear_q4(C.addressof(W), ptr(slot_of), ptr(x), dtype_code(x), T, E, k, ptr(offsets),
-                                   ptr(sorted_tok), ptr(active), act, ptr(out), dtype_code(out), ptr(dev_status),
-                                   stream_handle(stream)))
+    dev, P = _place_of(W.tensors[0]), T * k
+    code = lib.moe_expert_linear_q4(C.addressof(W), _table(slot_of, E, dev),
+                                    _address(x, (P if sorted_tok is None else T) * W.K, dev), dtype_code(x), T, E, k,
+                                    _table(offsets, E + 1, dev), _table(sorted_tok, P, dev),
+                                    _table(active, E + 1, dev), act,
+                                    _address(out, P * W.N // (1 + (act == ACT_SWIGLU)), dev), dtype_code(out),
+                                    _table(dev_status, 1, dev), stream_handle(stream))
+    if code:
+        raise MoeError("moe_expert_linear_q4", code)
 
 
 def expert_gemm(a, W, T: int, E: int, k: int, N: int, K: int, offsets, sorted_tok, out, dev_status=None,
                 stream=None) -> None:
     """out[s] = W[e] a_s for the sorted pairs s of every expert e
     (a_s = a[sorted_tok[s]], or a[s] with sorted_tok None)."""
-    P = T * k
-    _same_place((a, (P if sorted_tok is None else T) * K), (W, E * N * K), (offsets, E + 1), (sorted_tok, P),
-                (out, P * N), (dev_status, 1))
-    _int32(offsets, sorted_tok, dev_status)
-    dt = dtype_code(a)
+    dev, P, dt = _place_of(W), T * k, dtype_code(a)
     if dtype_code(W) != dt:
         raise ValueError("a and W have one type")
-    check("moe_expert_gemm", lib.moe_expert_gemm(ptr(a), ptr(W), dt, T, E, k, N, K, ptr(offsets), ptr(sorted_tok),
-                                                 ptr(out), dtype_code(out), ptr(dev_status), stream_handle(stream)))
+    code = lib.moe_expert_gemm(_address(a, (P if sorted_tok is None else T) * K, dev), _address(W, E * N * K, dev), dt,
+                               T, E, k, N, K, _table(offsets, E + 1, dev), _table(sorted_tok, P, dev),
+                               _address(out, P * N, dev), dtype_code(out), _table(dev_status, 1, dev),
+                               stream_handle(stream))
+    if code:
+        raise MoeError("moe_expert_gemm", code)
 
 
 def expert_gemm_dgrad(dy, W, T: int, E: int, k: int, N: int, K: int, offsets, da, dev_status=None,
                       stream=None) -> None:
     """da[s] = W[e]^T dy[s] for the sorted pairs s of every expert e."""
-    P = T * k
-    _same_place((dy, P * N), (W, E * N * K), (offsets, E + 1), (da, P * K), (dev_status, 1))
-    _int32(offsets, dev_status)
-    dt = dtype_code(dy)
+    dev, P, dt = _place_of(W), T * k, dtype_code(dy)
     if dtype_code(W) != dt:
         raise ValueError("dy and W have one type")
-    check("moe_expert_gemm_dgrad",
-          lib.moe_expert_gemm_dgrad(ptr(dy), ptr(W), dt, T, E, k, N, K, ptr(offsets), ptr(da), dtype_code(da),
-                                    ptr(dev_status), stream_handle(stream)))
+    code = lib.moe_expert_gemm_dgrad(_address(dy, P * N, dev), _address(W, E * N * K, dev), dt, T, E, k, N, K,
+                                     _table(offsets, E + 1, dev), _address(da, P * K, dev), dtype_code(da),
+                                     _table(dev_status, 1, dev), stream_handle(stream))
+    if code:
+        raise MoeError("moe_expert_gemm_dgrad", code)
 
 
 def expert_gemm_wgrad(dy, a, T: int, E: int, k: int, N: int, K: int, offsets, sorted_tok, dW, base=None,
                       dev_status=None, stream=None) -> None:
     """dW[e] = base[e] + sum over expert e's sorted pairs s of dy[s] a_s^T (base
     None: zeros; base may be dW)."""
-    P = T * k
-    _same_place((dy, P * N), (a, (P if sorted_tok is None else T) * K), (offsets, E + 1), (sorted_tok, P),
-                (dW, E * N * K), (base, E * N * K), (dev_status, 1))
-    _int32(offsets, sorted_tok, dev_status)
-    dt, odt = dtype_code(dy), dtype_code(dW)
+    dev, P, dt, odt = _place_of(dW), T * k, dtype_code(dy), dtype_code(dW)
     if dtype_code(a) != dt or (base is not None and dtype_code(base) != odt):
         raise ValueError("dy and a have one type, base and dW have one type")
-    check("moe_expert_gemm_wgrad",
-          lib.moe_expert_gemm_wgrad(ptr(dy), ptr(a), dt, T, E, k, N, K, ptr(offsets), ptr(sorted_tok), ptr(base),
-                                    ptr(dW), odt, ptr(dev_status), stream_handle(stream)))
+    code = lib.moe_expert_gemm_wgrad(_address(dy, P * N, dev), _address(a, (P if sorted_tok is None else T) * K, dev),
+                                     dt, T, E, k, N, K, _table(offsets, E + 1, dev), _table(sorted_tok, P, dev),
+                                     None if base is None else _address(base, E * N * K, dev),
+                                     _address(dW, E * N * K, dev), odt, _table(dev_status, 1, dev),
+                                     stream_handle(stream))
+    if code:
+        raise MoeError("moe_expert_gemm_wgrad", code)
 
 
 def swiglu(gu, rows: int, f: int, h, stream=None) -> None:
     """h = silu(g) * u for rows [g | u] of gu."""
-    _same_place((gu, rows * 2 * f), (h, rows * f))
-    dt = dtype_code(gu)
+    dev, dt = _place_of(gu), dtype_code(gu)
     if dtype_code(h) != dt:
         raise ValueError("gu and h have one type")
-    check("moe_swiglu", lib.moe_swiglu(ptr(gu), dt, rows, f, ptr(h), stream_handle(stream)))
+    code = lib.moe_swiglu(_address(gu, rows * 2 * f, dev), dt, rows, f, _address(h, rows * f, dev),
+                          stream_handle(stream))
+    if code:
+        raise MoeError("moe_swiglu", code)
 
 
 def swiglu_backward(gu, dh, rows: int, f: int, dgu, stream=None) -> None:
     """dgu = the gradient of swiglu to [g | u], given dh."""
-    _same_place((gu, rows * 2 * f), (dh, rows * f), (dgu, rows * 2 * f))
-    dt = dtype_code(gu)
+    dev, dt = _place_of(gu), dtype_code(gu)
     if dtype_code(dh) != dt or dtype_code(dgu) != dt:
         raise ValueError("gu, dh and dgu have one type")
-    check("moe_swiglu_backward", lib.moe_swiglu_backward(ptr(gu), ptr(dh), dt, rows, f, ptr(dgu),
-                                                         stream_handle(stream)))
+    code = lib.moe_swiglu_backward(_address(gu, rows * 2 * f, dev), _address(dh, rows * f, dev), dt, rows, f,
+                                   _address(dgu, rows * 2 * f, dev), stream_handle(stream))
+    if code:
+        raise MoeError("moe_swiglu_backward", code)
