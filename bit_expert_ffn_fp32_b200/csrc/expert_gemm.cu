@@ -39,9 +39,7 @@ enum Pass { kForward = 0, kDgrad = 1, kWgrad = 2 };
 constexpr int kTileM = 128;      // rows of tensor memory of a CTA
 constexpr int kTileI = 64;       // contracted index a stage: 128 bytes, one swizzle row
 constexpr int kLoadWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 8, kPickWarp0 = kEpiWarp0 + kEpiWarps;
-constexpr int kPickWarps = 8, kPickGroups = 2;  // gathering warps; stages they fill at the same time
-constexpr int kPickThreads = 32 * kPickWarps / kPickGroups;
-constexpr int kRelayWarp = kPickWarp0 + kPickWarps;
+constexpr int kPickThreads = 128;  // gathering threads that fill a stage
 constexpr int kMaxStages = 10;
 constexpr int kTurn = 2048;      // per epilogue warp: 32 x 32 16-bit values on their way to 16-byte stores
 constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
@@ -56,37 +54,49 @@ struct GemmParams {
     int M, I;        // extent of the output's contiguous index; of the contracted one (forward, dgrad)
     int N;           // wgrad: extent of the output's other index
     int bf16, out_fp32;
+    int stages;      // of the shared-memory ring
+    int blocks2;     // 1: MN-major operands are mapped in 64-wide blocks, two a box (extents multiples of 64)
     int32_t *status;
 };
 
-// Tensor maps. w: weights [E][N][K]; rows, rows16: 64- and 16-row boxes of the
-// rows that are N (forward, dgrad) or M (wgrad); dy: wgrad's other operand.
+// Tensor maps. w: weights [E][N][K]; rows: the rows that are N (forward, dgrad)
+// in boxes of 16, 32, 64, 96 and 128 rows, so that a tile's are one load; rows[0]
+// of wgrad: the rows that are M; dy: wgrad's other operand.
+constexpr int kBoxes = 5;
+__host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 16 : 32 * i; }
 struct GemmMaps {
-    CUtensorMap w, rows, rows16, dy;
+    CUtensorMap w, rows[kBoxes], dy;
+};
+
+// One expert that has tiles: its first tile, rows and id.
+struct Entry {
+    int tile, r0, rows, e;
 };
 
 struct GemmSmem {
     uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages], tfull[2], tempty[2];
     uint32_t tmem_base;
-    int abort;
-    int warp_sum[kRelayWarp + 1];
-    int prefix[kMaxE + 1];  // tiles before expert e
+    int abort, entries;
+    int warp_tiles[32], warp_entries[32];
 };
 
-// CG: CTAs that share a tile; TN: columns of a tile; PICK: with gathering warps.
-template <int PASS_, int CG_, int TN_, bool PICK_>
+// CG: CTAs that share a tile; TN: columns of a tile; PICK: groups of gathering
+// warps, stages they fill at the same time (0: none).
+template <int PASS_, int CG_, int TN_, int PICK_>
 struct Cfg {
-    static constexpr int PASS = PASS_, CG = CG_, TN = TN_;
-    static constexpr bool PICK = PICK_;
+    static constexpr int PASS = PASS_, CG = CG_, TN = TN_, PICK = PICK_;
+    static constexpr int kRelayWarp = kPickWarp0 + PICK * kPickThreads / 32;
     static constexpr int kThreads = 32 * (PICK ? kRelayWarp + 1 : kPickWarp0);
     static constexpr int kBRows = TN / CG;  // of B a CTA holds
     static constexpr int kA = kTileM * 128, kB = kBRows * 128, kStage = kA + kB;
-    // what fits beside the tables in 227 KB
-    static constexpr int kFit = (232448 - int(sizeof(GemmSmem)) - 1024 - kEpiWarps * kTurn) / kStage;
-    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-    static constexpr int kSmem = kStages * kStage + kEpiWarps * kTurn + 1024;
+    // shared memory: the ring, the epilogue's turning space, the table of E + 1 entries
+    static constexpr size_t fixed(int E) { return kEpiWarps * kTurn + (size_t(E) + 1) * sizeof(Entry) + 1024; }
+    static constexpr int stages(int E) {
+        const size_t fit = (232448 - 1024 - fixed(E)) / kStage;  // 1 KB: GemmSmem
+        return fit < size_t(kMaxStages) ? int(fit) : kMaxStages;
+    }
     static constexpr int kCols = 2 * TN;    // tensor memory: two accumulators
-    static_assert(kStages >= 4 && kCols >= 32 && kCols <= 512, "tile does not fit");
+    static_assert(stages(kMaxE) >= 4 && sizeof(GemmSmem) <= 1024 && kCols >= 32 && kCols <= 512, "tile does not fit");
 };
 
 __device__ __forceinline__ void stop(GemmSmem &s, int32_t *status) {
@@ -94,82 +104,111 @@ __device__ __forceinline__ void stop(GemmSmem &s, int32_t *status) {
 }
 
 // Rows of expert e; empty where the table is out of bounds.
-__device__ __forceinline__ bool range_of(const GemmParams &p, int e, int &r0, int &r1) {
-    r0 = p.offsets[e], r1 = p.offsets[e + 1];
-    if (r0 >= 0 && r1 >= r0 && r1 <= p.P) return true;
-    r0 = r1 = 0;
-    return false;
+__device__ __forceinline__ bool range_of(const GemmParams &p, int e, int &r0, int &rows) {
+    r0 = p.offsets[e];
+    const int r1 = p.offsets[e + 1];
+    const bool ok = r0 >= 0 && r1 >= r0 && r1 <= p.P;
+    rows = ok ? r1 - r0 : 0;
+    return ok;
 }
 
-// Whole CTA: prefix sums of the experts' tiles; returns their total.
 template <typename C>
-__device__ int build_prefix(const GemmParams &p, GemmSmem &s, int MT) {
+__device__ __forceinline__ int tiles_of(const GemmParams &p, int rows, int MT) {
+    if (C::PASS != kWgrad) return MT * ((rows + C::TN - 1) / C::TN);
+    // an expert without rows: nothing to do where the sum so far is in place
+    return rows > 0 || p.base != p.out ? MT * ((p.N + C::TN - 1) / C::TN) : 0;
+}
+
+// Whole CTA: the experts that have tiles, in order, and a last entry with the
+// number of all tiles, which is returned.
+template <typename C>
+__device__ int build_table(const GemmParams &p, GemmSmem &s, Entry *table, int MT) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.E + C::kThreads - 1) / C::kThreads, e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
-    int sum = 0;
+    int tiles = 0, entries = 0, r0, rows;
     for (int e = e0; e < e1; ++e) {
-        int r0, r1;
-        if (!range_of(p, e, r0, r1) && blockIdx.x == 0) flag(p.status, MOE_DEV_BAD_INDEX);
-        s.prefix[e] = sum;
-        if (C::PASS != kWgrad) sum += MT * ((r1 - r0 + C::TN - 1) / C::TN);
-        // an expert without rows: nothing to do where the sum so far is in place
-        else if (r1 > r0 || p.base != p.out) sum += MT * ((p.N + C::TN - 1) / C::TN);
+        if (!range_of(p, e, r0, rows) && blockIdx.x == 0) flag(p.status, MOE_DEV_BAD_INDEX);
+        const int n = tiles_of<C>(p, rows, MT);
+        tiles += n;
+        entries += n > 0;
     }
-    int incl = sum;
+    int t_incl = tiles, n_incl = entries;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int t = __shfl_up_sync(0xffffffffu, t_incl, o), n = __shfl_up_sync(0xffffffffu, n_incl, o);
+        if (lane >= o) t_incl += t, n_incl += n;
     }
-    if (lane == 31) s.warp_sum[warp] = incl;
+    if (lane == 31) s.warp_tiles[warp] = t_incl, s.warp_entries[warp] = n_incl;
     __syncthreads();
-    int before = incl - sum, total = 0;
+    int tile = t_incl - tiles, at = n_incl - entries, total = 0, all = 0;
     for (int w = 0; w < C::kThreads / 32; ++w) {
-        if (w < warp) before += s.warp_sum[w];
-        total += s.warp_sum[w];
+        const int t = s.warp_tiles[w], n = s.warp_entries[w];
+        if (w < warp) tile += t, at += n;
+        total += t, all += n;
     }
-    for (int e = e0; e < e1; ++e) s.prefix[e] += before;
-    if (tid == 0) s.prefix[p.E] = total;
-    __syncthreads();
+    for (int e = e0; e < e1; ++e) {
+        range_of(p, e, r0, rows);
+        const int n = tiles_of<C>(p, rows, MT);
+        if (n > 0) table[at++] = {tile, r0, rows, e};
+        tile += n;
+    }
+    if (tid == 0) {
+        table[all] = {total, 0, 0, 0};
+        s.entries = all;
+    }
     return total;
 }
 
 struct Tile {
     int e, m0;       // expert; first M index of this CTA
     int c0, n;       // forward, dgrad: first sorted pair and pairs; wgrad: first n and their number
-    int r0, r1;      // the expert's rows
+    int r0, rows;    // the expert's rows
     int npad, b0;    // n padded to the MMA's 16; first of the npad / CG of them whose B rows this CTA loads
 };
 
+// A warp's way through this CTA's tiles.
 template <typename C>
-__device__ __forceinline__ Tile tile_at(const GemmParams &p, const GemmSmem &s, int tau, int MT, int rank) {
-    int lo = 0, hi = p.E;  // last e with prefix[e] <= tau; experts without tiles share the next one's prefix
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s.prefix[mid] <= tau) lo = mid; else hi = mid;
+struct Walk {
+    const Entry *table;
+    int entries, MT, rank, at = 0;
+    float inv_mt;
+    __device__ Walk(const GemmSmem &s, const Entry *table, int MT, int rank)
+        : table(table), entries(s.entries), MT(MT), rank(rank), inv_mt(1.0f / MT) {}
+    // Tile tau, not before the last one asked for. All lanes together.
+    __device__ __forceinline__ Tile tile(const GemmParams &p, int tau) {
+        for (;;) {  // each lane looks at one of the next 32 entries
+            const int ahead = at + 1 + (threadIdx.x & 31);
+            const unsigned past = __ballot_sync(0xffffffffu, ahead < entries && table[min(ahead, entries)].tile <= tau);
+            at += __popc(past);
+            if (past != 0xffffffffu) break;
+        }
+        const Entry x = table[at];
+        Tile t;
+        t.e = x.e, t.r0 = x.r0, t.rows = x.rows;
+        const int local = tau - x.tile;
+        int j = int(float(local) * inv_mt);  // local / MT, off by one at most
+        j += (j + 1) * MT <= local;
+        j -= j * MT > local;
+        t.m0 = ((local - j * MT) * C::CG + rank) * kTileM;
+        if (C::PASS == kWgrad) {
+            t.c0 = j * C::TN;
+            t.n = min(C::TN, p.N - t.c0);
+        } else {  // the rows spread evenly over their tiles, in multiples of 16
+            const int nt = (t.rows + C::TN - 1) / C::TN;
+            const int per = nt == 1 ? C::TN : ((t.rows + nt - 1) / nt + 15) & ~15;
+            t.c0 = t.r0 + j * per;
+            t.n = min(per, t.r0 + t.rows - t.c0);
+        }
+        // in 64-wide blocks, each CTA of a pair takes whole ones
+        t.npad = C::PASS == kWgrad && p.blocks2 ? (t.n + 127) & ~127 : (t.n + 15) & ~15;
+        t.b0 = rank * (t.npad / C::CG);
+        return t;
     }
-    Tile t;
-    t.e = lo;
-    range_of(p, lo, t.r0, t.r1);
-    const int local = tau - s.prefix[lo], j = local / MT;
-    t.m0 = ((local - j * MT) * C::CG + rank) * kTileM;
-    if (C::PASS == kWgrad) {
-        t.c0 = j * C::TN;
-        t.n = min(C::TN, p.N - t.c0);
-    } else {  // the rows spread evenly over their tiles, in multiples of 16
-        const int rows = t.r1 - t.r0, nt = (rows + C::TN - 1) / C::TN;
-        const int per = ((rows + nt - 1) / nt + 15) & ~15;
-        t.c0 = t.r0 + j * per;
-        t.n = min(per, t.r1 - t.c0);
-    }
-    t.npad = (t.n + 15) & ~15;
-    t.b0 = rank * (t.npad / C::CG);
-    return t;
-}
+};
 
 template <typename C>
 __device__ __forceinline__ int stages_of(const GemmParams &p, const Tile &t) {
-    return ((C::PASS == kWgrad ? t.r1 - t.r0 : p.I) + kTileI - 1) / kTileI;
+    return ((C::PASS == kWgrad ? t.rows : p.I) + kTileI - 1) / kTileI;
 }
 
 // MN-major operand, 128-byte swizzle: blocks of 64 along MN 8192 bytes apart
@@ -180,12 +219,12 @@ __device__ __forceinline__ uint64_t desc_mn128(uint32_t saddr) {
 }
 
 // Position in the ring of stages.
-template <typename C>
 struct Ring {
-    int stage = 0;
+    int stages, stage = 0;
     uint32_t phase = 0;
+    __device__ explicit Ring(int stages) : stages(stages) {}
     __device__ __forceinline__ void next() {
-        if (++stage == C::kStages) {
+        if (++stage == stages) {
             stage = 0;
             phase ^= 1;
         }
@@ -195,9 +234,8 @@ struct Ring {
 // TMA warp: fills stage after stage, all tiles of this CTA in a row. The bytes
 // of both CTAs of a pair count on rank 0's barrier.
 template <typename C>
-__device__ void load_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &m, unsigned char *dyn, int total, int MT,
-                           int rank) {
-    Ring<C> at;
+__device__ void load_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &m, unsigned char *dyn, Walk<C> walk, int total) {
+    Ring at(p.stages);
     int it = 0;
     bool ok = true;
     const uint32_t full0 = C::CG == 2 ? tc::at_rank(tc::smem_u32(&s.full[0]), 0) : tc::smem_u32(&s.full[0]);
@@ -210,21 +248,28 @@ __device__ void load_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &m, 
         if (C::CG == 2) tc::tma_load_3d_pair(dst, map, x, y, z, bar);
         else tc::tma_load_3d_at(dst, map, x, y, z, bar);
     };
+    auto load4 = [](uint32_t dst, const void *map, int x, int y, int z, int w, uint32_t bar) {
+        if (C::CG == 2) tc::tma_load_4d_pair(dst, map, x, y, z, w, bar);
+        else tc::tma_load_4d_at(dst, map, x, y, z, w, bar);
+    };
     for (int tau = blockIdx.x / C::CG; tau < total && ok; tau += gridDim.x / C::CG) {
-        const Tile t = tile_at<C>(p, s, tau, MT, rank);
+        const Tile t = walk.tile(p, tau);
         const int KS = stages_of<C>(p, t);
         // 64-wide blocks of an MN-major A that lie inside the tensor (none for a
-        // CTA whose rows all lie past it), and the same of both CTAs of a pair
-        const int ablocks = max(0, min(2, (p.M - t.m0 + 63) / 64));
-        const int ablocks_all = min(2 * C::CG, (p.M - (t.m0 - rank * kTileM) + 63) / 64);
-        // rows of B: boxes of 64, a short rest in boxes of 16 (the same in both CTAs)
-        const int brows = t.npad / C::CG, rest = brows & 63, brow0 = t.c0 + t.b0;
-        const int box64 = brows / 64 + (rest > 32), box16 = rest > 32 ? 0 : (rest + 15) / 16;
-        const int bblocks = (brows + 63) / 64;  // wgrad: 64-wide blocks of n
+        // CTA whose rows all lie past it), and the same of both CTAs of a pair;
+        // a box of two counts whole
+        const int rank = walk.rank, mfirst = t.m0 - rank * kTileM;
+        int ablocks = max(0, min(2, (p.M - t.m0 + 63) / 64)), ablocks_all = min(2 * C::CG, (p.M - mfirst + 63) / 64);
+        if (p.blocks2) ablocks_all += ablocks_all & 1, ablocks += ablocks & 1;
+        // rows of B in one box (the same in both CTAs); wgrad: 64-wide blocks of n
+        const int brows = t.npad / C::CG, brow0 = t.c0 + t.b0;
+        const int box = brows <= 16 ? 0 : (brows + 31) / 32;
+        int bblocks = (brows + 63) / 64;
+        if (p.blocks2) bblocks += bblocks & 1;
         // bytes of a stage of both CTAs
         const uint32_t bytes_a = C::PASS == kForward ? C::CG * C::kA : ablocks_all * 8192;
         const uint32_t bytes_b = C::PASS == kWgrad ? C::CG * bblocks * 8192
-                                                   : C::PICK ? 0 : C::CG * (box64 * 8192 + box16 * 2048);
+                                                   : C::PICK ? 0 : C::CG * box_rows(box) * 128;
         for (int ks = 0; ks < KS; ++ks, ++it, at.next()) {
             if (!tc::mbar_wait_warp(&s.empty[at.stage], at.phase ^ 1, kWaitNs)) {
                 ok = false;
@@ -233,35 +278,30 @@ __device__ void load_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &m, 
             const uint32_t a = dyn0 + at.stage * C::kStage, b = a + C::kA, bar = full0 + at.stage * 8;
             const int i0 = kTileI * ks;
             // wgrad's last stage of an expert, and its rows by token, come from the gathering warps
-            const bool load_b = C::PASS == kWgrad ? t.r1 - t.r0 - i0 >= kTileI : !C::PICK;
+            const bool load_b = C::PASS == kWgrad ? t.rows - i0 >= kTileI : !C::PICK;
             const bool load_a = C::PASS != kWgrad || (load_b && !p.sorted_tok);
             if (tc::elect_one()) {
                 if (rank == 0)
                     tc::mbar_arrive_expect_tx(&s.full[at.stage], (load_a ? bytes_a : 0) + (load_b ? bytes_b : 0));
                 if (C::PASS == kForward) {
                     load3(a, &m.w, i0, t.m0, t.e, bar);
+                } else if (load_a && p.blocks2) {
+                    if (ablocks) {
+                        if (C::PASS == kDgrad) load4(a, &m.w, 0, i0, t.m0 / 64, t.e, bar);
+                        else load3(a, &m.rows[0], 0, t.r0 + i0, t.m0 / 64, bar);
+                    }
                 } else if (load_a) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (i < ablocks) {
-                            if (C::PASS == kDgrad) load3(a + 8192 * i, &m.w, t.m0 + 64 * i, i0, t.e, bar);
-                            else load2(a + 8192 * i, &m.rows, t.m0 + 64 * i, t.r0 + i0, bar);
-                        }
+                    for (int i = 0; i < ablocks; ++i) {
+                        if (C::PASS == kDgrad) load3(a + 8192 * i, &m.w, t.m0 + 64 * i, i0, t.e, bar);
+                        else load2(a + 8192 * i, &m.rows[0], t.m0 + 64 * i, t.r0 + i0, bar);
+                    }
                 }
                 if (C::PASS == kWgrad && load_b) {
-#pragma unroll
-                    for (int i = 0; i < C::kBRows / 64; ++i)
-                        if (i < bblocks) load2(b + 8192 * i, &m.dy, brow0 + 64 * i, t.r0 + i0, bar);
+                    if (p.blocks2) load3(b, &m.dy, 0, t.r0 + i0, brow0 / 64, bar);
+                    else
+                        for (int i = 0; i < bblocks; ++i) load2(b + 8192 * i, &m.dy, brow0 + 64 * i, t.r0 + i0, bar);
                 }
-                if (C::PASS != kWgrad && !C::PICK) {
-#pragma unroll
-                    for (int i = 0; i < C::kBRows / 64; ++i)
-                        if (i < box64) load2(b + 8192 * i, &m.rows, i0, brow0 + 64 * i, bar);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (i < box16)
-                            load2(b + box64 * 8192 + 2048 * i, &m.rows16, i0, brow0 + box64 * 64 + 16 * i, bar);
-                }
+                if (C::PASS != kWgrad && !C::PICK) load2(b, &m.rows[box], i0, brow0, bar);
             }
             __syncwarp();
         }
@@ -269,9 +309,9 @@ __device__ void load_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &m, 
     if (!ok) {
         stop(s, p.status);
         // no copy may land after this CTA's shared memory has another owner
-        if (rank == 0)
-            for (int i = max(0, it - C::kStages); i < it; ++i)
-                tc::mbar_wait(&s.full[i % C::kStages], (i / C::kStages) & 1, kWaitNs);
+        if (walk.rank == 0)
+            for (int i = max(0, it - p.stages); i < it; ++i)
+                tc::mbar_wait(&s.full[i % p.stages], (i / p.stages) & 1, kWaitNs);
     }
 }
 
@@ -291,15 +331,15 @@ __device__ __forceinline__ int picked_row(const GemmParams &p, int pair, int end
 
 // Gathering warps: forward's rows by token (K-major B); wgrad's rows by token
 // (MN-major A) and, in an expert's last stage, the rows of both operands. Four
-// warps fill a stage, the two groups of four every second one. They never wait
+// warps fill a stage; two groups of four take every second one. They never wait
 // for their copies: those arrive on `landed` by themselves, so that a whole ring
 // of stages is in flight, and the relay warp hands the stage to the MMA.
 template <typename C>
-__device__ void gather_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn, int total, int MT, int rank) {
+__device__ void gather_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn, Walk<C> walk, int total) {
     const int tid = (threadIdx.x - 32 * kPickWarp0) % kPickThreads;
     const int group = (threadIdx.x - 32 * kPickWarp0) / kPickThreads;
     const uint32_t dyn0 = tc::smem_u32(dyn);
-    Ring<C> at;
+    Ring at(p.stages);
     int it = 0;
     bool ok = true;
     // this thread's chunk of 16 bytes in its rows, and its place in a stage: rows
@@ -309,7 +349,7 @@ __device__ void gather_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dy
     const int ch = tid % kCh, row0 = tid / kCh;
     const uint32_t off = (ch >> 3) * 8192 + row0 * 128 + (((ch & 7) ^ (row0 & 7)) << 4);
     for (int tau = blockIdx.x / C::CG; tau < total && ok; tau += gridDim.x / C::CG) {
-        const Tile t = tile_at<C>(p, s, tau, MT, rank);
+        const Tile t = walk.tile(p, tau);
         const int KS = stages_of<C>(p, t), brows = t.npad / C::CG;
         const uint16_t *from[kRows];  // this thread's chunk in each of its rows, NULL: zeros
         if (C::PASS == kForward) {
@@ -321,17 +361,18 @@ __device__ void gather_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dy
             }
         }
         const bool picks = C::PASS == kForward || p.sorted_tok;
+        const int end = t.r0 + t.rows;
         const int m = t.m0 + 8 * ch;
         int row[kRows];  // wgrad: rows of the next stage this thread fills
         auto next_rows = [&](int ks) {
             const int first = t.r0 + kTileI * ks;
-            if (ks < KS && (p.sorted_tok || t.r1 - first < kTileI))
+            if (ks < KS && (p.sorted_tok || end - first < kTileI))
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) row[i] = picked_row(p, first + row0 + kApart * i, t.r1);
+                for (int i = 0; i < kRows; ++i) row[i] = picked_row(p, first + row0 + kApart * i, end);
         };
-        if (C::PASS == kWgrad) next_rows((it + group) & 1);
+        if (C::PASS == kWgrad) next_rows(C::PICK == 2 ? (it + group) & 1 : 0);
         for (int ks = 0; ks < KS; ++ks, ++it, at.next()) {
-            if ((it & 1) != group) continue;
+            if (C::PICK == 2 && (it & 1) != group) continue;
             if (!tc::mbar_wait_warp(&s.empty[at.stage], at.phase ^ 1, kWaitNs)) {
                 ok = false;
                 break;
@@ -347,7 +388,7 @@ __device__ void gather_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dy
                     cp_async16_or_zero(b + off + i * (kApart * 128), in ? from[i] + k : p.rows, in);
                 }
             } else {
-                const int first = t.r0 + kTileI * ks, left = t.r1 - first;
+                const int first = t.r0 + kTileI * ks, left = end - first;
                 const bool tail = left < kTileI;
                 const int rows = tail ? (left + 15) & ~15 : kTileI;
                 if (tail || picks) {
@@ -371,7 +412,7 @@ __device__ void gather_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dy
                                            in);
                     }
                 }
-                next_rows(ks + 2);
+                next_rows(ks + C::PICK);
             }
             tc::cp_async_arrive_noinc(&s.landed[at.stage]);
         }
@@ -383,12 +424,12 @@ __device__ void gather_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dy
 // Relay warp: a stage whose gathered rows have landed is made visible to the
 // tensor cores and counted on rank 0's barrier.
 template <typename C>
-__device__ void relay_stages(const GemmParams &p, GemmSmem &s, int total, int MT, int rank) {
+__device__ void relay_stages(const GemmParams &p, GemmSmem &s, Walk<C> walk, int total) {
     const uint32_t full0 = C::CG == 2 ? tc::at_rank(tc::smem_u32(&s.full[0]), 0) : tc::smem_u32(&s.full[0]);
-    Ring<C> at;
+    Ring at(p.stages);
     bool ok = true;
     for (int tau = blockIdx.x / C::CG; tau < total && ok; tau += gridDim.x / C::CG) {
-        const int KS = stages_of<C>(p, tile_at<C>(p, s, tau, MT, rank));
+        const int KS = stages_of<C>(p, walk.tile(p, tau));
         for (int ks = 0; ks < KS; ++ks, at.next()) {
             if (!tc::mbar_wait_warp(&s.landed[at.stage], at.phase, kWaitNs)) {
                 ok = false;
@@ -403,7 +444,8 @@ __device__ void relay_stages(const GemmParams &p, GemmSmem &s, int total, int MT
 }
 
 template <typename C>
-__device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, int total, int MT, uint32_t tmem) {
+__device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, Walk<C> walk, int total,
+                          uint32_t tmem) {
     constexpr bool kMnA = C::PASS != kForward, kMnB = C::PASS == kWgrad;
     // descriptors advance by 16 of the contracted index: 32 bytes in a K-major row, 16 rows of an MN-major block
     constexpr uint64_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
@@ -421,11 +463,11 @@ __device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, 
         if (C::CG == 2) tc::mma_commit_pair(bar);
         else tc::mma_commit(bar);
     };
-    Ring<C> at;
+    Ring at(p.stages);
     int count = 0;
     bool ok = true;
     for (int tau = blockIdx.x / C::CG; tau < total && ok && !s.abort; tau += gridDim.x / C::CG) {
-        const Tile t = tile_at<C>(p, s, tau, MT, 0);
+        const Tile t = walk.tile(p, tau);
         const int KS = stages_of<C>(p, t);
         if (KS == 0) continue;  // wgrad of an expert without rows
         const int buf = count & 1;
@@ -437,7 +479,7 @@ __device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, 
         ++count;
         const uint32_t idesc = idesc0 | (uint32_t(t.npad >> 3) << 17);
         const uint32_t d = tmem + uint32_t(buf * C::TN);
-        int left = C::PASS == kWgrad ? t.r1 - t.r0 : p.I;
+        int left = C::PASS == kWgrad ? t.rows : p.I;
         for (int ks = 0; ks < KS; ++ks, left -= kTileI, at.next()) {
             if (!tc::mbar_wait_warp(&s.full[at.stage], at.phase, kWaitNs)) {
                 ok = false;
@@ -446,11 +488,15 @@ __device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, 
             tc::fence_after();
             const uint64_t a = a0 + uint32_t(at.stage * (C::kStage >> 4)), b = b0 + uint32_t(at.stage * (C::kStage >> 4));
             if (tc::elect_one()) {
-                // steps of 16; the last one reads zeros past the end
                 mma(d, a, b, idesc, ks ? 1u : 0u);
-                if (left > 16) mma(d, a + kStepA, b + kStepB, idesc, 1u);
-                if (left > 32) mma(d, a + 2 * kStepA, b + 2 * kStepB, idesc, 1u);
-                if (left > 48) mma(d, a + 3 * kStepA, b + 3 * kStepB, idesc, 1u);
+                if (left > 48) {
+                    mma(d, a + kStepA, b + kStepB, idesc, 1u);
+                    mma(d, a + 2 * kStepA, b + 2 * kStepB, idesc, 1u);
+                    mma(d, a + 3 * kStepA, b + 3 * kStepB, idesc, 1u);
+                } else {  // steps of 16; the last one reads zeros past the end
+                    if (left > 16) mma(d, a + kStepA, b + kStepB, idesc, 1u);
+                    if (left > 32) mma(d, a + 2 * kStepA, b + 2 * kStepB, idesc, 1u);
+                }
                 commit(&s.empty[at.stage]);
                 if (ks == KS - 1) commit(&s.tfull[buf]);
             }
@@ -460,23 +506,14 @@ __device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, 
     if (!ok) stop(s, p.status);
 }
 
-// 32 x 32 accumulators (lanes M, columns) to 16-bit rows of 32 M values: loaded
-// as mma fragments, packed along the columns, turned by the transposing matrix
-// store into this warp's 2 KB ([column][32], 16-byte chunks swizzled against
-// bank conflicts), read back and written as 16-byte pieces.
+// 32 x 32 accumulators (lanes M, columns), as fragments v of two 16-lane
+// halves, to 16-bit rows of 32 M values: packed along the columns, turned by the
+// transposing matrix store into this warp's 2 KB ([column][32], 16-byte chunks
+// swizzled against bank conflicts), read back and written as 16-byte pieces.
 template <typename O>
-__device__ __forceinline__ void turn_and_store(uint32_t td, bool sums, uint32_t turn, O *out, int64_t pitch, int cols,
-                                               int m_left) {
+__device__ __forceinline__ void turn_and_store(const uint32_t (&v)[2][16], uint32_t turn, O *out, int64_t pitch,
+                                               int cols, int m_left) {
     const int lane = threadIdx.x & 31;
-    uint32_t v[2][16];
-    if (sums) {
-        tc::tmem_ld16x256_x4_nowait(td, v[0]);
-        tc::tmem_ld16x256_x4_nowait(td + (16u << 16), v[1]);
-        tc::tmem_ld_wait();
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0u;
-    }
     __syncwarp();  // the chunks of the last 32 columns have been read
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -492,16 +529,18 @@ __device__ __forceinline__ void turn_and_store(uint32_t td, bool sums, uint32_t 
         tc::stmatrix_x4_trans(turn + n * 64 + ((ch ^ ((n >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
-    const int ch = lane & 3;
+    const int ch = lane & 3, n0 = lane >> 2;
+    O *to = out + n0 * pitch + 8 * ch;
+    const bool in = 8 * ch < m_left;
+    uint4 r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = 8 * i + (lane >> 2);
-        uint4 r;
+    for (int i = 0; i < 4; ++i)  // columns 8 apart have the same swizzle
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                     : "r"(turn + n * 64 + ((ch ^ ((n >> 1) & 3)) << 4)));
-        if (n < cols && 8 * ch < m_left) *reinterpret_cast<uint4 *>(out + n * pitch + 8 * ch) = r;
-    }
+                     : "=r"(r[i].x), "=r"(r[i].y), "=r"(r[i].z), "=r"(r[i].w)
+                     : "r"(turn + n0 * 64 + ((ch ^ ((n0 >> 1) & 3)) << 4) + i * 512));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (in && n0 + 8 * i < cols) *reinterpret_cast<uint4 *>(to + 8 * i * pitch) = r[i];
 }
 
 // Epilogue warps: lane quadrant warp % 4 of tensor memory, every second 32
@@ -511,16 +550,16 @@ __device__ __forceinline__ void turn_and_store(uint32_t td, bool sums, uint32_t 
 // so that each lane holds two neighbours of one column), the sum read 32 columns
 // ahead of its use, the first 32 while the products still run.
 template <typename C, typename O>
-__device__ void store_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn, int total, int MT, uint32_t tmem,
-                            int rank) {
+__device__ void store_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn, Walk<C> walk, int total,
+                            uint32_t tmem) {
     constexpr bool kAdd = C::PASS == kWgrad, kWide = sizeof(O) == 4;
     constexpr int kVals = kWide ? 32 : 16;  // 32-bit words a lane stores of 32 columns
     const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = threadIdx.x & 31;
     const int q = (warp + kEpiWarp0) & 3, half = warp >> 2, odd = lane & 1;
-    const uint32_t turn = tc::smem_u32(dyn) + C::kStages * C::kStage + warp * kTurn;
+    const uint32_t turn = tc::smem_u32(dyn) + p.stages * C::kStage + warp * kTurn;
     int count = 0;
     for (int tau = blockIdx.x / C::CG; tau < total && !s.abort; tau += gridDim.x / C::CG) {
-        const Tile t = tile_at<C>(p, s, tau, MT, rank);
+        const Tile t = walk.tile(p, tau);
         const bool sums = stages_of<C>(p, t) > 0;
         const int m = t.m0 + 32 * q + lane;
         const bool in = m < p.M;
@@ -539,7 +578,7 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn
         if (kAdd && p.base && 32 * half < t.n) read_old(32 * half);
         const int buf = count & 1;
         if (sums) {
-            if (!tc::mbar_wait_sleep(&s.tfull[buf], (count >> 1) & 1, kWaitNs, 32)) {
+            if (!tc::mbar_wait(&s.tfull[buf], (count >> 1) & 1, kWaitNs)) {
                 stop(s, p.status);
                 break;
             }
@@ -547,14 +586,35 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn
             ++count;
         }
         const uint32_t td = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * C::TN);
-        for (int c = 32 * half; c < t.n; c += 64) {
-            if constexpr (!kWide)
-                if (!(kAdd && p.base)) {
-                    const int m1 = t.m0 + 32 * q;
-                    turn_and_store<O>(td + c, sums, turn, static_cast<O *>(p.out) + (row0 + c) * p.M + m1, p.M,
-                                      t.n - c, p.M - m1);
-                    continue;
+        bool stored = false;
+        if constexpr (!kWide)
+            if (!(kAdd && p.base)) {
+                const int m1 = t.m0 + 32 * q;
+                O *o = static_cast<O *>(p.out) + row0 * p.M + m1;
+                uint32_t v[2][2][16];  // the next 32 columns are on their way while these are stored
+                auto fetch = [&](int c, uint32_t(&f)[2][16]) {
+                    if (sums && c < t.n) {
+                        tc::tmem_ld16x256_x4_nowait(td + c, f[0]);
+                        tc::tmem_ld16x256_x4_nowait(td + c + (16u << 16), f[1]);
+                    }
+                };
+                if (!sums)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[0][0][i] = v[0][1][i] = v[1][0][i] = v[1][1][i] = 0u;
+                fetch(32 * half, v[0]);
+                for (int c = 32 * half; c < t.n; c += 128) {
+                    tc::tmem_ld_wait();
+                    fetch(c + 64, v[1]);
+                    turn_and_store<O>(v[0], turn, o + int64_t(c) * p.M, p.M, t.n - c, p.M - m1);
+                    if (c + 64 < t.n) {
+                        tc::tmem_ld_wait();
+                        fetch(c + 128, v[0]);
+                        turn_and_store<O>(v[1], turn, o + int64_t(c + 64) * p.M, p.M, t.n - c - 64, p.M - m1);
+                    }
                 }
+                stored = true;
+            }
+        for (int c = 32 * half; c < t.n && !stored; c += 64) {
             uint32_t v[32];
             if (sums) {
                 tc::tmem_ld32_nowait(td + c, v);
@@ -616,7 +676,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int rank = C::CG == 2 ? int(tc::cluster_rank()) : 0;
     const int MT = (p.M + kTileM * C::CG - 1) / (kTileM * C::CG);
     if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
+        for (int i = 0; i < p.stages; ++i) {
             tc::mbar_init(&s.full[i], 1 + (C::PICK ? C::CG : 0));
             tc::mbar_init(&s.empty[i], 1);
             tc::mbar_init(&s.landed[i], kPickThreads);
@@ -632,27 +692,29 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (C::CG == 2) tc::tmem_alloc_pair(&s.tmem_base, C::kCols);
         else tc::tmem_alloc(&s.tmem_base, C::kCols);
     }
-    const int total = build_prefix<C>(p, s, MT);
+    Entry *table = reinterpret_cast<Entry *>(dyn + p.stages * C::kStage + kEpiWarps * kTurn);
+    const int total = build_table<C>(p, s, table, MT);
     tc::fence_before();
     if (C::CG == 2) tc::cluster_sync();  // both CTAs' barriers are set up
     else __syncthreads();
     tc::fence_after();
     const uint32_t tmem = s.tmem_base;
+    const Walk<C> walk(s, table, MT, rank);
     if (warp == kLoadWarp) {
-        load_tiles<C>(p, s, maps, dyn, total, MT, rank);
+        load_tiles<C>(p, s, maps, dyn, walk, total);
     } else if (warp == kMmaWarp) {
-        if (rank == 0) issue_mma<C>(p, s, dyn, total, MT, tmem);
+        if (rank == 0) issue_mma<C>(p, s, dyn, walk, total, tmem);
     } else if (warp >= kPickWarp0) {
         if constexpr (C::PICK) {
-            if (warp == kRelayWarp) relay_stages<C>(p, s, total, MT, rank);
-            else gather_tiles<C>(p, s, dyn, total, MT, rank);
+            if (warp == C::kRelayWarp) relay_stages<C>(p, s, walk, total);
+            else gather_tiles<C>(p, s, dyn, walk, total);
         }
     } else if (p.out_fp32) {
-        store_tiles<C, float>(p, s, dyn, total, MT, tmem, rank);
+        store_tiles<C, float>(p, s, dyn, walk, total, tmem);
     } else if (p.bf16) {
-        store_tiles<C, __nv_bfloat16>(p, s, dyn, total, MT, tmem, rank);
+        store_tiles<C, __nv_bfloat16>(p, s, dyn, walk, total, tmem);
     } else {
-        store_tiles<C, __half>(p, s, dyn, total, MT, tmem, rank);
+        store_tiles<C, __half>(p, s, dyn, walk, total, tmem);
     }
     __syncwarp();
     tc::fence_before();
@@ -690,21 +752,37 @@ bool host_setup(int &sms) {
     return true;
 }
 
-// 16-bit tensor [slabs][rows][inner] in boxes of box_rows x 64, 128-byte swizzle, zeros outside.
-bool map16(CUtensorMap *m, bool bf16, const void *base, int64_t inner, int64_t rows, int64_t slabs, uint32_t box_rows) {
-    const cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(slabs)};
-    const cuuint64_t strides[2] = {cuuint64_t(inner) * 2, cuuint64_t(inner) * cuuint64_t(rows) * 2};
-    const cuuint32_t box[3] = {64, box_rows, 1};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, slabs ? 3 : 2,
-                    const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+// 16-bit tensor of up to 4 dimensions (innermost first, strides in elements) in
+// boxes of 64 x box_rows x ..., 128-byte swizzle, zeros outside.
+bool map16(CUtensorMap *m, bool bf16, const void *base, int rank, const int64_t (&extent)[4], const int64_t (&stride)[4],
+           const uint32_t (&box)[4]) {
+    cuuint64_t dims[4], strides[3];
+    cuuint32_t b[4], es[4];
+    for (int i = 0; i < rank; ++i) {
+        dims[i] = cuuint64_t(extent[i]);
+        if (i) strides[i - 1] = cuuint64_t(stride[i]) * 2;
+        b[i] = box[i];
+        es[i] = 1;
+    }
+    return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                    const_cast<void *>(base), dims, strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// rows x inner, boxes of box_rows x 64.
+bool map_rows(CUtensorMap *m, bool bf16, const void *base, int64_t inner, int64_t rows, int box_rows) {
+    return map16(m, bf16, base, 2, {inner, rows, 1, 1}, {1, inner, 0, 0}, {64, uint32_t(box_rows), 1, 1});
+}
+// rows x inner as 64-wide blocks (inner a multiple of 64), boxes of two blocks x 64 rows.
+bool map_blocks(CUtensorMap *m, bool bf16, const void *base, int64_t inner, int64_t rows) {
+    return map16(m, bf16, base, 3, {64, rows, inner / 64, 1}, {1, inner, 64, 0}, {64, 64, 2, 1});
+}
 
 template <typename C>
-moe_status launch(const GemmParams &p, const GemmMaps &maps, int64_t most_tiles, int sms, cudaStream_t stream) {
-    if (cudaFuncSetAttribute(expert_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
+moe_status launch(GemmParams &p, const GemmMaps &maps, int64_t most_tiles, int sms, cudaStream_t stream) {
+    p.stages = C::stages(p.E);
+    const size_t smem = p.stages * C::kStage + C::fixed(p.E);
+    if (cudaFuncSetAttribute(expert_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
         cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
@@ -712,7 +790,7 @@ moe_status launch(const GemmParams &p, const GemmMaps &maps, int64_t most_tiles,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(sms / C::CG, most_tiles)) * C::CG);
     cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -734,34 +812,45 @@ moe_status run_gemm(int pass, GemmParams &p, const void *w, int N, int K, cudaSt
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
-    GemmMaps maps = {};
+    GemmMaps maps;
     const bool bf = p.bf16, pick = p.sorted_tok != nullptr;
-    const int inner = pass == kDgrad ? N : K;
+    const int64_t experts = std::min<int64_t>(p.E, p.P);
+    // Few rows an expert: the weights' bytes bound the call, so tiles are narrow
+    // and single, with more stages of weights in flight and more of them.
+    const bool narrow = pass != kWgrad && p.P <= 16 * experts;
+    // One box of two blocks instead of two loads (90 cycles of the issuing
+    // thread each), where the extent along MN has no ragged last block.
+    p.blocks2 = pass == kWgrad ? N % 64 == 0 && K % 64 == 0 : pass == kDgrad && K % 64 == 0;
     bool ok = true;
     if (p.P > 0) {  // an empty batch (wgrad) has no rows to describe, and loads none
-        if (!pick)
-            ok = map16(&maps.rows, bf, p.rows, inner, p.rows_a, 0, 64) &&
-                 (pass == kWgrad || map16(&maps.rows16, bf, p.rows, inner, p.rows_a, 0, 16));
-        if (pass == kWgrad) ok = ok && map16(&maps.dy, bf, p.dy, N, p.P, 0, 64);
-        else ok = ok && map16(&maps.w, bf, w, K, N, p.E, pass == kForward ? 128 : 64);
+        if (pass == kForward)
+            ok = map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 128, 1, 1});
+        else if (pass == kDgrad)
+            ok = p.blocks2 ? map16(&maps.w, bf, w, 4, {64, N, K / 64, p.E}, {1, K, 64, int64_t(N) * K}, {64, 64, 2, 1})
+                           : map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 64, 1, 1});
+        else
+            ok = p.blocks2 ? map_blocks(&maps.dy, bf, p.dy, N, p.P) : map_rows(&maps.dy, bf, p.dy, N, p.P, 64);
+        if (!pick && pass == kWgrad)
+            ok = ok && (p.blocks2 ? map_blocks(&maps.rows[0], bf, p.rows, K, p.rows_a)
+                                  : map_rows(&maps.rows[0], bf, p.rows, K, p.rows_a, 64));
+        if (!pick && pass != kWgrad)
+            for (int i = 0; i < (narrow ? 2 : kBoxes); ++i)
+                ok = ok && map_rows(&maps.rows[i], bf, p.rows, p.I, p.rows_a, box_rows(i));
     }
     if (!ok) return MOE_ERR_CUDA;
     const int64_t MT1 = (p.M + kTileM - 1) / kTileM, MT2 = (MT1 + 1) / 2;
     if (pass == kWgrad)
-        return launch<Cfg<kWgrad, 2, 256, true>>(p, maps, MT2 * ((N + 255) / 256) * p.E, sms, stream);
-    // Few rows an expert: the weights' bytes bound the call, so tiles are narrow
-    // and single, with more stages of weights in flight and more of them.
-    const int64_t experts = std::min<int64_t>(p.E, p.P);
-    if (p.P <= 16 * experts) {
+        return launch<Cfg<kWgrad, 2, 256, 1>>(p, maps, MT2 * ((N + 255) / 256) * p.E, sms, stream);
+    if (narrow) {
         const int64_t most = MT1 * (experts + p.P / 32);
-        if (pass == kDgrad) return launch<Cfg<kDgrad, 1, 32, false>>(p, maps, most, sms, stream);
-        return pick ? launch<Cfg<kForward, 1, 32, true>>(p, maps, most, sms, stream)
-                    : launch<Cfg<kForward, 1, 32, false>>(p, maps, most, sms, stream);
+        if (pass == kDgrad) return launch<Cfg<kDgrad, 1, 32, 0>>(p, maps, most, sms, stream);
+        return pick ? launch<Cfg<kForward, 1, 32, 2>>(p, maps, most, sms, stream)
+                    : launch<Cfg<kForward, 1, 32, 0>>(p, maps, most, sms, stream);
     }
     const int64_t most = MT2 * (experts + p.P / 256);
-    if (pass == kDgrad) return launch<Cfg<kDgrad, 2, 256, false>>(p, maps, most, sms, stream);
-    return pick ? launch<Cfg<kForward, 2, 256, true>>(p, maps, most, sms, stream)
-                : launch<Cfg<kForward, 2, 256, false>>(p, maps, most, sms, stream);
+    if (pass == kDgrad) return launch<Cfg<kDgrad, 2, 256, 0>>(p, maps, most, sms, stream);
+    return pick ? launch<Cfg<kForward, 2, 256, 2>>(p, maps, most, sms, stream)
+                : launch<Cfg<kForward, 2, 256, 0>>(p, maps, most, sms, stream);
 }
 
 moe_status check_gemm(int dtype, int T, int E, int k, int N, int K, int out_dtype) {
@@ -784,8 +873,8 @@ MOE_API moe_status moe_expert_gemm(const void *a, const void *W, int dtype, int 
     const moe_status st = check_gemm(dtype, T, E, k, N, K, out_dtype);
     if (st != MOE_OK || T == 0) return st;
     if (!a || !W || !offsets || !out || !aligned16(a) || !aligned16(W) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
-    GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), nullptr, nullptr, out,
-                    sorted_tok ? T : T * k, T * k, E, N, K, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, dev_status};
+    GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), nullptr, nullptr, out, sorted_tok ? T : T * k,
+                    T * k, E, N, K, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, dev_status};
     return run_gemm(kForward, p, W, N, K, as_cuda(stream));
 }
 
@@ -796,7 +885,7 @@ MOE_API moe_status moe_expert_gemm_dgrad(const void *dy, const void *W, int dtyp
     if (st != MOE_OK || T == 0) return st;
     if (!dy || !W || !offsets || !da || !aligned16(dy) || !aligned16(W) || !aligned16(da)) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, nullptr, static_cast<const uint16_t *>(dy), nullptr, nullptr, da,
-                    T * k, T * k, E, K, N, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, dev_status};
+                    T * k, T * k, E, K, N, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, dev_status};
     return run_gemm(kDgrad, p, W, N, K, as_cuda(stream));
 }
 
@@ -808,6 +897,7 @@ MOE_API moe_status moe_expert_gemm_wgrad(const void *dy, const void *a, int dtyp
     if (!offsets || !dW || !aligned16(dW) || !aligned16(base)) return MOE_ERR_INVALID_ARG;
     if (T > 0 && (!dy || !a || !aligned16(dy) || !aligned16(a))) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), static_cast<const uint16_t *>(dy), base, dW,
-                    sorted_tok ? T : T * k, T * k, E, K, 0, N, dtype == MOE_BF16, out_dtype == MOE_FP32, dev_status};
+                    sorted_tok ? T : T * k, T * k, E, K, 0, N, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0,
+                    dev_status};
     return run_gemm(kWgrad, p, nullptr, N, K, as_cuda(stream));
 }

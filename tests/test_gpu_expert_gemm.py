@@ -66,6 +66,7 @@ SHAPES = [
     (1000, 1, 1, 392, 1096, 0.0),
     (257, 16, 300, 256, 136, 0.1),
     (64, 10, 512, 1536, 256, 0.0),
+    (300, 16, 4096, 64, 192, 0.5),   # as many experts as there may be
 ]
 
 
