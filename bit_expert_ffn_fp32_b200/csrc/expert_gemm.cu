@@ -61,11 +61,12 @@ struct GemmParams {
 
 // Tensor maps. w: weights [E][N][K]; rows: the rows that are N (forward, dgrad)
 // in boxes of 16, 32, 64, 96 and 128 rows, so that a tile's are one load; rows[0]
-// of wgrad: the rows that are M; dy: wgrad's other operand.
+// of wgrad: the rows that are M; dy: wgrad's other operand; out: the result, in
+// boxes of 32 M and 32 (16-bit) or 16 (fp32) columns.
 constexpr int kBoxes = 5;
 __host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 16 : 32 * i; }
 struct GemmMaps {
-    CUtensorMap w, rows[kBoxes], dy;
+    CUtensorMap w, rows[kBoxes], dy, out;
 };
 
 // One expert that has tiles: its first tile, rows and id.
@@ -506,15 +507,17 @@ __device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, 
     if (!ok) stop(s, p.status);
 }
 
+// Epilogue warps: lane quadrant warp % 4 of tensor memory, every second 32
+// columns. Results pass through this warp's 2 KB of shared memory and leave as
+// TMA boxes of 32 M and 32 columns (fp32: 16), those of a tile's ragged end as
+// plain stores: a box would reach the next expert's rows.
+
 // 32 x 32 accumulators (lanes M, columns), as fragments v of two 16-lane
-// halves, to 16-bit rows of 32 M values: packed along the columns, turned by the
-// transposing matrix store into this warp's 2 KB ([column][32], 16-byte chunks
-// swizzled against bank conflicts), read back and written as 16-byte pieces.
+// halves, to [column][32] in 16 bits: packed along the columns, turned by the
+// transposing matrix store, 16-byte chunks in the 64-byte swizzle.
 template <typename O>
-__device__ __forceinline__ void turn_and_store(const uint32_t (&v)[2][16], uint32_t turn, O *out, int64_t pitch,
-                                               int cols, int m_left) {
+__device__ __forceinline__ void turn16(const uint32_t (&v)[2][16], uint32_t turn) {
     const int lane = threadIdx.x & 31;
-    __syncwarp();  // the chunks of the last 32 columns have been read
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t w[4];
@@ -528,55 +531,190 @@ __device__ __forceinline__ void turn_and_store(const uint32_t (&v)[2][16], uint3
         const int n = 8 * i + (lane & 7), ch = lane >> 3;
         tc::stmatrix_x4_trans(turn + n * 64 + ((ch ^ ((n >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
     }
-    __syncwarp();
-    const int ch = lane & 3, n0 = lane >> 2;
-    O *to = out + n0 * pitch + 8 * ch;
-    const bool in = 8 * ch < m_left;
-    uint4 r[4];
+}
+// Columns below `cols` of them to memory, 16 bytes a lane.
+template <typename O>
+__device__ __forceinline__ void store16(uint32_t turn, O *out, int64_t pitch, int cols, int m_left) {
+    const int lane = threadIdx.x & 31, ch = lane & 3, n0 = lane >> 2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // columns 8 apart have the same swizzle
+    for (int i = 0; i < 4; ++i) {  // columns 8 apart have the same swizzle
+        uint4 r;
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r[i].x), "=r"(r[i].y), "=r"(r[i].z), "=r"(r[i].w)
+                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                      : "r"(turn + n0 * 64 + ((ch ^ ((n0 >> 1) & 3)) << 4) + i * 512));
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (in && n0 + 8 * i < cols) *reinterpret_cast<uint4 *>(to + 8 * i * pitch) = r[i];
+        if (8 * ch < m_left && n0 + 8 * i < cols) *reinterpret_cast<uint4 *>(out + (n0 + 8 * i) * pitch + 8 * ch) = r;
+    }
 }
 
-// Epilogue warps: lane quadrant warp % 4 of tensor memory, every second 32
-// columns. 16-bit output goes through turn_and_store; fp32 output as a column's
-// 32 consecutive values at a time. With a sum so far (wgrad), 16-bit output is
-// rounded only after the addition: two columns at once (lane pairs swap values
-// so that each lane holds two neighbours of one column), the sum read 32 columns
-// ahead of its use, the first 32 while the products still run.
+// 16-bit results. The next 32 columns are on their way while these are stored.
 template <typename C, typename O>
-__device__ void store_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn, Walk<C> walk, int total,
-                            uint32_t tmem) {
-    constexpr bool kAdd = C::PASS == kWgrad, kWide = sizeof(O) == 4;
-    constexpr int kVals = kWide ? 32 : 16;  // 32-bit words a lane stores of 32 columns
+__device__ __forceinline__ void store_tile16(const GemmParams &p, const CUtensorMap &map, const Tile &t, bool sums,
+                                             uint32_t td, uint32_t turn, int half, int m1) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row0 = C::PASS == kWgrad ? int64_t(t.e) * p.N + t.c0 : int64_t(t.c0);
+    O *o = static_cast<O *>(p.out) + row0 * p.M + m1;
+    uint32_t v[2][2][16];
+    auto fetch = [&](int c, uint32_t(&f)[2][16]) {
+        if (sums && c < t.n) {
+            tc::tmem_ld16x256_x4_nowait(td + c, f[0]);
+            tc::tmem_ld16x256_x4_nowait(td + c + (16u << 16), f[1]);
+        }
+    };
+    auto store = [&](int c, const uint32_t(&f)[2][16]) {
+        if (lane == 0) tc::bulk_wait_read<0>();
+        __syncwarp();  // the columns before have left the buffer
+        turn16<O>(f, turn);
+        if (C::PASS == kWgrad || c + 32 <= t.n) {
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && m1 < p.M) {
+                tc::tma_store_3d(&map, m1, t.c0 + c, C::PASS == kWgrad ? t.e : 0, turn);
+                tc::bulk_commit();
+            }
+        } else {
+            __syncwarp();
+            store16<O>(turn, o + int64_t(c) * p.M, p.M, t.n - c, p.M - m1);
+        }
+    };
+    if (!sums)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[0][0][i] = v[0][1][i] = v[1][0][i] = v[1][1][i] = 0u;
+    fetch(32 * half, v[0]);
+    for (int c = 32 * half; c < t.n; c += 128) {
+        tc::tmem_ld_wait();
+        fetch(c + 64, v[1]);
+        store(c, v[0]);
+        if (c + 64 < t.n) {
+            tc::tmem_ld_wait();
+            fetch(c + 128, v[0]);
+            store(c + 64, v[1]);
+        }
+    }
+}
+
+// fp32 results, 16 columns at a time; into a sum that is in place by the
+// reduction of the boxes, which adds them where they land.
+template <typename C>
+__device__ __forceinline__ void store_tile32(const GemmParams &p, const CUtensorMap &map, const Tile &t, bool sums,
+                                             uint32_t td, uint32_t turn, int half, int m1) {
+    const int lane = threadIdx.x & 31, m = m1 + lane;
+    const bool add = C::PASS == kWgrad && p.base;
+    float *o = static_cast<float *>(p.out) + (C::PASS == kWgrad ? int64_t(t.e) * p.N + t.c0 : int64_t(t.c0)) * p.M + m;
+    for (int c = 32 * half; c < t.n; c += 64) {
+        uint32_t v[32];
+        if (sums) {
+            tc::tmem_ld32_nowait(td + c, v);
+            tc::tmem_ld_wait();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c1 = c + 16 * h;
+            if (c1 >= t.n) break;
+            if (C::PASS == kWgrad || c1 + 16 <= t.n) {
+                if (lane == 0) tc::bulk_wait_read<0>();
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(turn + i * 128 + lane * 4), "r"(v[16 * h + i]) : "memory");
+                tc::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0 && m1 < p.M) {
+                    if (add) tc::tma_add_3d(&map, m1, t.c0 + c1, t.e, turn);
+                    else tc::tma_store_3d(&map, m1, t.c0 + c1, C::PASS == kWgrad ? t.e : 0, turn);
+                    tc::bulk_commit();
+                }
+            } else if (m < p.M) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c1 + i < t.n) o[int64_t(c1 + i) * p.M] = __uint_as_float(v[16 * h + i]);
+            }
+        }
+    }
+}
+
+// wgrad onto a sum that is elsewhere (or in 16 bits, which are rounded only
+// after the addition): read and added here. fp32: a column's 32 consecutive
+// values at a time; 16 bits: two columns at once (lane pairs swap values so that
+// each lane holds two neighbours of one column). The first 32 columns of the
+// sum are read while the products still run, the others 32 ahead of their use.
+template <typename C, typename O>
+struct AddTile {
+    static constexpr bool kWide = sizeof(O) == 4;
+    static constexpr int kVals = kWide ? 32 : 16;  // 32-bit words a lane stores of 32 columns
+    uint32_t old[kVals];
+    int64_t at0;
+    bool in;
+    int odd;
+    __device__ __forceinline__ void read(const GemmParams &p, const Tile &t, int c) {
+        const O *b = static_cast<const O *>(p.base) + at0 + int64_t(c) * p.M;
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) {
+            const int col = kWide ? i : 2 * i;
+            old[i] = in && c + col + (kWide ? 0 : odd) < t.n
+                         ? *reinterpret_cast<const uint32_t *>(b + int64_t(col) * p.M) : 0u;
+        }
+    }
+    __device__ __forceinline__ void begin(const GemmParams &p, const Tile &t, int half, int m1) {
+        const int m = m1 + (threadIdx.x & 31);
+        odd = threadIdx.x & 1;
+        in = m < p.M;
+        const int64_t row0 = int64_t(t.e) * p.N + t.c0;
+        // word i of 32 columns from c: fp32 column c + i; 16 bits column c + 2 i + odd, elements m & ~1 and next
+        at0 = kWide ? row0 * p.M + m : (row0 + odd) * p.M + (m & ~1);
+        if (32 * half < t.n) read(p, t, 32 * half);
+    }
+    __device__ __forceinline__ void store(const GemmParams &p, const Tile &t, bool sums, uint32_t td, int half) {
+        for (int c = 32 * half; c < t.n; c += 64) {
+            uint32_t v[32], word[kVals];
+            if (sums) {
+                tc::tmem_ld32_nowait(td + c, v);
+                tc::tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < kVals; ++i) {
+                if (kWide) {
+                    word[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(old[i]));
+                } else {
+                    const uint32_t a = v[(2 * i) & 31], b = v[(2 * i + 1) & 31];
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                    const O *o = reinterpret_cast<const O *>(&old[i]);
+                    const O pair[2] = {from_f32<O>(__uint_as_float(odd ? got : a) + to_f32(o[0])),
+                                       from_f32<O>(__uint_as_float(odd ? b : got) + to_f32(o[1]))};
+                    word[i] = *reinterpret_cast<const uint32_t *>(pair);
+                }
+            }
+            if (c + 64 < t.n) read(p, t, c + 64);
+            O *o = static_cast<O *>(p.out) + at0 + int64_t(c) * p.M;
+#pragma unroll
+            for (int i = 0; i < kVals; ++i) {
+                const int col = kWide ? i : 2 * i;
+                if (in && c + col + (kWide ? 0 : odd) < t.n)
+                    *reinterpret_cast<uint32_t *>(o + int64_t(col) * p.M) = word[i];
+            }
+        }
+    }
+};
+
+template <typename C, typename O>
+__device__ void store_tiles(const GemmParams &p, GemmSmem &s, const CUtensorMap &map, unsigned char *dyn, Walk<C> walk,
+                            int total, uint32_t tmem) {
     const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = threadIdx.x & 31;
-    const int q = (warp + kEpiWarp0) & 3, half = warp >> 2, odd = lane & 1;
+    const int q = (warp + kEpiWarp0) & 3, half = warp >> 2;
     const uint32_t turn = tc::smem_u32(dyn) + p.stages * C::kStage + warp * kTurn;
+    const bool read_base = C::PASS == kWgrad && p.base && (sizeof(O) == 2 || p.base != p.out);
     int count = 0;
     for (int tau = blockIdx.x / C::CG; tau < total && !s.abort; tau += gridDim.x / C::CG) {
         const Tile t = walk.tile(p, tau);
         const bool sums = stages_of<C>(p, t) > 0;
-        const int m = t.m0 + 32 * q + lane;
-        const bool in = m < p.M;
-        const int64_t row0 = C::PASS == kWgrad ? int64_t(t.e) * p.N + t.c0 : int64_t(t.c0);
-        // word i of 32 columns from c: fp32 column c + i; 16 bits column c + 2 i + odd, elements m & ~1 and next
-        const int64_t at0 = kWide ? row0 * p.M + m : (row0 + odd) * p.M + (m & ~1);
-        const int step = kWide ? 1 : 2, first = kWide ? 0 : odd;
-        uint32_t old[kAdd ? kVals : 1];
-        auto read_old = [&](int c) {
-            const O *b = static_cast<const O *>(p.base) + at0 + int64_t(c) * p.M;
-#pragma unroll
-            for (int i = 0; i < kVals; ++i)
-                old[kAdd ? i : 0] = in && c + step * i + first < t.n
-                                        ? *reinterpret_cast<const uint32_t *>(b + int64_t(step * i) * p.M) : 0u;
-        };
-        if (kAdd && p.base && 32 * half < t.n) read_old(32 * half);
-        const int buf = count & 1;
+        const int m1 = t.m0 + 32 * q, buf = count & 1;
+        AddTile<C, O> sum;
+        if (read_base) sum.begin(p, t, half, m1);
         if (sums) {
             if (!tc::mbar_wait(&s.tfull[buf], (count >> 1) & 1, kWaitNs)) {
                 stop(s, p.status);
@@ -585,75 +723,11 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn
             tc::fence_after();
             ++count;
         }
+        __syncwarp();
         const uint32_t td = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * C::TN);
-        bool stored = false;
-        if constexpr (!kWide)
-            if (!(kAdd && p.base)) {
-                const int m1 = t.m0 + 32 * q;
-                O *o = static_cast<O *>(p.out) + row0 * p.M + m1;
-                uint32_t v[2][2][16];  // the next 32 columns are on their way while these are stored
-                auto fetch = [&](int c, uint32_t(&f)[2][16]) {
-                    if (sums && c < t.n) {
-                        tc::tmem_ld16x256_x4_nowait(td + c, f[0]);
-                        tc::tmem_ld16x256_x4_nowait(td + c + (16u << 16), f[1]);
-                    }
-                };
-                if (!sums)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[0][0][i] = v[0][1][i] = v[1][0][i] = v[1][1][i] = 0u;
-                fetch(32 * half, v[0]);
-                for (int c = 32 * half; c < t.n; c += 128) {
-                    tc::tmem_ld_wait();
-                    fetch(c + 64, v[1]);
-                    turn_and_store<O>(v[0], turn, o + int64_t(c) * p.M, p.M, t.n - c, p.M - m1);
-                    if (c + 64 < t.n) {
-                        tc::tmem_ld_wait();
-                        fetch(c + 128, v[0]);
-                        turn_and_store<O>(v[1], turn, o + int64_t(c + 64) * p.M, p.M, t.n - c - 64, p.M - m1);
-                    }
-                }
-                stored = true;
-            }
-        for (int c = 32 * half; c < t.n && !stored; c += 64) {
-            uint32_t v[32];
-            if (sums) {
-                tc::tmem_ld32_nowait(td + c, v);
-                tc::tmem_ld_wait();
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0u;
-            }
-            uint32_t word[kVals];
-            if (kWide) {
-#pragma unroll
-                for (int i = 0; i < kVals; ++i) {
-                    word[i] = v[i];
-                    if (kAdd && p.base)
-                        word[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(old[kAdd ? i : 0]));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kVals; ++i) {
-                    const uint32_t mine = odd ? v[(2 * i + 1) & 31] : v[(2 * i) & 31];
-                    const uint32_t got =
-                        __shfl_xor_sync(0xffffffffu, odd ? v[(2 * i) & 31] : v[(2 * i + 1) & 31], 1);
-                    float lo = __uint_as_float(odd ? got : mine), hi = __uint_as_float(odd ? mine : got);
-                    if (kAdd && p.base) {
-                        const O *o = reinterpret_cast<const O *>(&old[kAdd ? i : 0]);
-                        lo += to_f32(o[0]);
-                        hi += to_f32(o[1]);
-                    }
-                    O pair[2] = {from_f32<O>(lo), from_f32<O>(hi)};
-                    word[i] = *reinterpret_cast<const uint32_t *>(pair);
-                }
-            }
-            if (kAdd && p.base && c + 64 < t.n) read_old(c + 64);
-            O *o = static_cast<O *>(p.out) + at0 + int64_t(c) * p.M;
-#pragma unroll
-            for (int i = 0; i < kVals; ++i)
-                if (in && c + step * i + first < t.n)
-                    *reinterpret_cast<uint32_t *>(o + int64_t(step * i) * p.M) = word[i];
-        }
+        if (read_base) sum.store(p, t, sums, td, half);
+        else if constexpr (sizeof(O) == 2) store_tile16<C, O>(p, map, t, sums, td, turn, half, m1);
+        else store_tile32<C>(p, map, t, sums, td, turn, half, m1);
         if (sums) {
             tc::fence_before();
             __syncwarp();
@@ -663,6 +737,7 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, unsigned char *dyn
             }
         }
     }
+    if (lane == 0) tc::bulk_wait_read<0>();
 }
 
 template <typename C>
@@ -710,11 +785,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             else gather_tiles<C>(p, s, dyn, walk, total);
         }
     } else if (p.out_fp32) {
-        store_tiles<C, float>(p, s, dyn, walk, total, tmem);
+        store_tiles<C, float>(p, s, maps.out, dyn, walk, total, tmem);
     } else if (p.bf16) {
-        store_tiles<C, __nv_bfloat16>(p, s, dyn, walk, total, tmem);
+        store_tiles<C, __nv_bfloat16>(p, s, maps.out, dyn, walk, total, tmem);
     } else {
-        store_tiles<C, __half>(p, s, dyn, walk, total, tmem);
+        store_tiles<C, __half>(p, s, maps.out, dyn, walk, total, tmem);
     }
     __syncwarp();
     tc::fence_before();
@@ -753,7 +828,7 @@ bool host_setup(int &sms) {
 }
 
 // 16-bit tensor of up to 4 dimensions (innermost first, strides in elements) in
-// boxes of 64 x box_rows x ..., 128-byte swizzle, zeros outside.
+// boxes 64 wide, 128-byte swizzle, zeros outside.
 bool map16(CUtensorMap *m, bool bf16, const void *base, int rank, const int64_t (&extent)[4], const int64_t (&stride)[4],
            const uint32_t (&box)[4]) {
     cuuint64_t dims[4], strides[3];
@@ -767,6 +842,19 @@ bool map16(CUtensorMap *m, bool bf16, const void *base, int rank, const int64_t 
     return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
                     const_cast<void *>(base), dims, strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The result [slabs][rows][inner], boxes of 32 x 32 16-bit values (64-byte
+// swizzle) or 16 x 32 fp32 ones.
+bool map_out(CUtensorMap *m, bool bf16, bool fp32, const void *base, int64_t inner, int64_t rows, int64_t slabs) {
+    const cuuint64_t size = fp32 ? 4 : 2;
+    const cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(slabs)};
+    const cuuint64_t strides[2] = {cuuint64_t(inner) * size, cuuint64_t(inner) * cuuint64_t(rows) * size};
+    const cuuint32_t box[3] = {32, fp32 ? 16u : 32u, 1}, es[3] = {1, 1, 1};
+    return g_encode(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                            : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    3, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    fp32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // rows x inner, boxes of box_rows x 64.
@@ -821,15 +909,17 @@ moe_status run_gemm(int pass, GemmParams &p, const void *w, int N, int K, cudaSt
     // One box of two blocks instead of two loads (90 cycles of the issuing
     // thread each), where the extent along MN has no ragged last block.
     p.blocks2 = pass == kWgrad ? N % 64 == 0 && K % 64 == 0 : pass == kDgrad && K % 64 == 0;
-    bool ok = true;
+    bool ok = pass == kWgrad ? map_out(&maps.out, bf, p.out_fp32, p.out, K, N, p.E)
+                             : map_out(&maps.out, bf, p.out_fp32, p.out, p.M, p.P, 1);
     if (p.P > 0) {  // an empty batch (wgrad) has no rows to describe, and loads none
         if (pass == kForward)
-            ok = map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 128, 1, 1});
+            ok = ok && map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 128, 1, 1});
         else if (pass == kDgrad)
-            ok = p.blocks2 ? map16(&maps.w, bf, w, 4, {64, N, K / 64, p.E}, {1, K, 64, int64_t(N) * K}, {64, 64, 2, 1})
-                           : map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 64, 1, 1});
+            ok = ok && (p.blocks2
+                            ? map16(&maps.w, bf, w, 4, {64, N, K / 64, p.E}, {1, K, 64, int64_t(N) * K}, {64, 64, 2, 1})
+                            : map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 64, 1, 1}));
         else
-            ok = p.blocks2 ? map_blocks(&maps.dy, bf, p.dy, N, p.P) : map_rows(&maps.dy, bf, p.dy, N, p.P, 64);
+            ok = ok && (p.blocks2 ? map_blocks(&maps.dy, bf, p.dy, N, p.P) : map_rows(&maps.dy, bf, p.dy, N, p.P, 64));
         if (!pick && pass == kWgrad)
             ok = ok && (p.blocks2 ? map_blocks(&maps.rows[0], bf, p.rows, K, p.rows_a)
                                   : map_rows(&maps.rows[0], bf, p.rows, K, p.rows_a, 64));
