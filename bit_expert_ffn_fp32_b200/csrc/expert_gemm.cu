@@ -55,6 +55,7 @@ struct GemmParams {
     int N;           // wgrad: extent of the output's other index
     int bf16, out_fp32;
     int stages;      // of the shared-memory ring
+    int split;       // 1: an fp32 result is summed in several accumulators
     int blocks2;     // 1: MN-major operands are mapped in 64-wide blocks, two a box (extents multiples of 64)
     int32_t *status;
 };
@@ -96,7 +97,12 @@ struct Cfg {
         const size_t fit = (232448 - 1024 - fixed(E)) / kStage;  // 1 KB: GemmSmem
         return fit < size_t(kMaxStages) ? int(fit) : kMaxStages;
     }
-    static constexpr int kCols = 2 * TN;    // tensor memory: two accumulators
+    // Tensor memory: two buffers, so that the epilogue of one tile runs beside the
+    // products of the next. An fp32 result of a long sum is formed in kAccs
+    // accumulators, its stages in turn, added at the end: the tensor cores cut
+    // instead of round, an error that grows with the length of a chain. Narrow
+    // tiles have room for four in each buffer; wide ones take both buffers.
+    static constexpr int kAccs = CG == 1 ? 4 : 2, kBuf = CG == 1 ? kAccs * TN : TN, kCols = 2 * kBuf;
     static_assert(stages(kMaxE) >= 4 && sizeof(GemmSmem) <= 1024 && kCols >= 32 && kCols <= 512, "tile does not fit");
 };
 
@@ -210,6 +216,14 @@ struct Walk {
 template <typename C>
 __device__ __forceinline__ int stages_of(const GemmParams &p, const Tile &t) {
     return ((C::PASS == kWgrad ? t.rows : p.I) + kTileI - 1) / kTileI;
+}
+
+// Accumulator buffer, and the phase of its barriers, of a CTA's tile number count.
+template <typename C>
+__device__ __forceinline__ int buffer_of(const GemmParams &p, int count, uint32_t &phase) {
+    const bool one = C::CG == 2 && p.split;
+    phase = (one ? count : count >> 1) & 1;
+    return one ? 0 : count & 1;
 }
 
 // MN-major operand, 128-byte swizzle: blocks of 64 along MN 8192 bytes apart
@@ -471,15 +485,17 @@ __device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, 
         const Tile t = walk.tile(p, tau);
         const int KS = stages_of<C>(p, t);
         if (KS == 0) continue;  // wgrad of an expert without rows
-        const int buf = count & 1;
-        if (!tc::mbar_wait_warp(&s.tempty[buf], ((count >> 1) & 1) ^ 1, kWaitNs)) {
+        uint32_t phase;
+        const int buf = buffer_of<C>(p, count, phase);
+        if (!tc::mbar_wait_warp(&s.tempty[buf], phase ^ 1, kWaitNs)) {
             ok = false;
             break;
         }
         tc::fence_after();
         ++count;
         const uint32_t idesc = idesc0 | (uint32_t(t.npad >> 3) << 17);
-        const uint32_t d = tmem + uint32_t(buf * C::TN);
+        const uint32_t d0 = tmem + uint32_t(buf * C::kBuf);
+        const int accs = p.split ? C::kAccs : 1;
         int left = C::PASS == kWgrad ? t.rows : p.I;
         for (int ks = 0; ks < KS; ++ks, left -= kTileI, at.next()) {
             if (!tc::mbar_wait_warp(&s.full[at.stage], at.phase, kWaitNs)) {
@@ -488,8 +504,9 @@ __device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, 
             }
             tc::fence_after();
             const uint64_t a = a0 + uint32_t(at.stage * (C::kStage >> 4)), b = b0 + uint32_t(at.stage * (C::kStage >> 4));
+            const uint32_t d = d0 + uint32_t((ks & (accs - 1)) * C::TN);
             if (tc::elect_one()) {
-                mma(d, a, b, idesc, ks ? 1u : 0u);
+                mma(d, a, b, idesc, ks >= accs ? 1u : 0u);
                 if (left > 48) {
                     mma(d, a + kStepA, b + kStepB, idesc, 1u);
                     mma(d, a + 2 * kStepA, b + 2 * kStepB, idesc, 1u);
@@ -592,19 +609,32 @@ __device__ __forceinline__ void store_tile16(const GemmParams &p, const CUtensor
     }
 }
 
+// 32 columns of fp32, the sum of `accs` accumulators.
+template <typename C>
+__device__ __forceinline__ void fetch32(uint32_t td, int accs, uint32_t (&v)[32]) {
+    tc::tmem_ld32_nowait(td, v);
+    tc::tmem_ld_wait();
+    for (int a = 1; a < accs; ++a) {
+        uint32_t u[32];
+        tc::tmem_ld32_nowait(td + uint32_t(a * C::TN), u);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+    }
+}
+
 // fp32 results, 16 columns at a time; into a sum that is in place by the
 // reduction of the boxes, which adds them where they land.
 template <typename C>
-__device__ __forceinline__ void store_tile32(const GemmParams &p, const CUtensorMap &map, const Tile &t, bool sums,
+__device__ __forceinline__ void store_tile32(const GemmParams &p, const CUtensorMap &map, const Tile &t, int accs,
                                              uint32_t td, uint32_t turn, int half, int m1) {
     const int lane = threadIdx.x & 31, m = m1 + lane;
     const bool add = C::PASS == kWgrad && p.base;
     float *o = static_cast<float *>(p.out) + (C::PASS == kWgrad ? int64_t(t.e) * p.N + t.c0 : int64_t(t.c0)) * p.M + m;
     for (int c = 32 * half; c < t.n; c += 64) {
         uint32_t v[32];
-        if (sums) {
-            tc::tmem_ld32_nowait(td + c, v);
-            tc::tmem_ld_wait();
+        if (accs) {
+            fetch32<C>(td + c, accs, v);
         } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
@@ -666,12 +696,11 @@ struct AddTile {
         at0 = kWide ? row0 * p.M + m : (row0 + odd) * p.M + (m & ~1);
         if (32 * half < t.n) read(p, t, 32 * half);
     }
-    __device__ __forceinline__ void store(const GemmParams &p, const Tile &t, bool sums, uint32_t td, int half) {
+    __device__ __forceinline__ void store(const GemmParams &p, const Tile &t, int accs, uint32_t td, int half) {
         for (int c = 32 * half; c < t.n; c += 64) {
             uint32_t v[32], word[kVals];
-            if (sums) {
-                tc::tmem_ld32_nowait(td + c, v);
-                tc::tmem_ld_wait();
+            if (accs) {
+                fetch32<C>(td + c, accs, v);
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0u;
@@ -711,12 +740,13 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, const CUtensorMap 
     int count = 0;
     for (int tau = blockIdx.x / C::CG; tau < total && !s.abort; tau += gridDim.x / C::CG) {
         const Tile t = walk.tile(p, tau);
-        const bool sums = stages_of<C>(p, t) > 0;
-        const int m1 = t.m0 + 32 * q, buf = count & 1;
+        const int KS = stages_of<C>(p, t), accs = p.split ? min(C::kAccs, KS) : min(1, KS);  // 0: no sums
+        uint32_t phase;
+        const int m1 = t.m0 + 32 * q, buf = buffer_of<C>(p, count, phase);
         AddTile<C, O> sum;
         if (read_base) sum.begin(p, t, half, m1);
-        if (sums) {
-            if (!tc::mbar_wait(&s.tfull[buf], (count >> 1) & 1, kWaitNs)) {
+        if (accs) {
+            if (!tc::mbar_wait(&s.tfull[buf], phase, kWaitNs)) {
                 stop(s, p.status);
                 break;
             }
@@ -724,11 +754,11 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, const CUtensorMap 
             ++count;
         }
         __syncwarp();
-        const uint32_t td = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * C::TN);
-        if (read_base) sum.store(p, t, sums, td, half);
-        else if constexpr (sizeof(O) == 2) store_tile16<C, O>(p, map, t, sums, td, turn, half, m1);
-        else store_tile32<C>(p, map, t, sums, td, turn, half, m1);
-        if (sums) {
+        const uint32_t td = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * C::kBuf);
+        if (read_base) sum.store(p, t, accs, td, half);
+        else if constexpr (sizeof(O) == 2) store_tile16<C, O>(p, map, t, accs > 0, td, turn, half, m1);
+        else store_tile32<C>(p, map, t, accs, td, turn, half, m1);
+        if (accs) {
             tc::fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -906,6 +936,10 @@ moe_status run_gemm(int pass, GemmParams &p, const void *w, int N, int K, cudaSt
     // Few rows an expert: the weights' bytes bound the call, so tiles are narrow
     // and single, with more stages of weights in flight and more of them.
     const bool narrow = pass != kWgrad && p.P <= 16 * experts;
+    // Chains of more than 768: relative error 7e-7 there, where fp32 products summed
+    // in fp32 have 2e-7. (wgrad: by the rows an expert has on average.)
+    const int64_t chain = pass == kWgrad ? p.P / std::max<int64_t>(experts, 1) : p.I;
+    p.split = p.out_fp32 && (narrow || chain > 768);
     // One box of two blocks instead of two loads (90 cycles of the issuing
     // thread each), where the extent along MN has no ragged last block.
     p.blocks2 = pass == kWgrad ? N % 64 == 0 && K % 64 == 0 : pass == kDgrad && K % 64 == 0;
@@ -964,7 +998,7 @@ MOE_API moe_status moe_expert_gemm(const void *a, const void *W, int dtype, int 
     if (st != MOE_OK || T == 0) return st;
     if (!a || !W || !offsets || !out || !aligned16(a) || !aligned16(W) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), nullptr, nullptr, out, sorted_tok ? T : T * k,
-                    T * k, E, N, K, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, dev_status};
+                    T * k, E, N, K, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, dev_status};
     return run_gemm(kForward, p, W, N, K, as_cuda(stream));
 }
 
@@ -975,7 +1009,7 @@ MOE_API moe_status moe_expert_gemm_dgrad(const void *dy, const void *W, int dtyp
     if (st != MOE_OK || T == 0) return st;
     if (!dy || !W || !offsets || !da || !aligned16(dy) || !aligned16(W) || !aligned16(da)) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, nullptr, static_cast<const uint16_t *>(dy), nullptr, nullptr, da,
-                    T * k, T * k, E, K, N, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, dev_status};
+                    T * k, T * k, E, K, N, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, dev_status};
     return run_gemm(kDgrad, p, W, N, K, as_cuda(stream));
 }
 
@@ -987,7 +1021,7 @@ MOE_API moe_status moe_expert_gemm_wgrad(const void *dy, const void *a, int dtyp
     if (!offsets || !dW || !aligned16(dW) || !aligned16(base)) return MOE_ERR_INVALID_ARG;
     if (T > 0 && (!dy || !a || !aligned16(dy) || !aligned16(a))) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), static_cast<const uint16_t *>(dy), base, dW,
-                    sorted_tok ? T : T * k, T * k, E, K, 0, N, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0,
+                    sorted_tok ? T : T * k, T * k, E, K, 0, N, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0,
                     dev_status};
     return run_gemm(kWgrad, p, nullptr, N, K, as_cuda(stream));
 }
