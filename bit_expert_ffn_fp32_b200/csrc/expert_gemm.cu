@@ -55,6 +55,7 @@ struct GemmParams {
     int N;           // wgrad: extent of the output's other index
     int bf16, out_fp32;
     int stages;      // of the shared-memory ring
+    int read_base;   // 1: wgrad's sum so far is read (0: there is none, or the results are added where it is)
     int split;       // 1: an fp32 result is summed in several accumulators
     int blocks2;     // 1: MN-major operands are mapped in 64-wide blocks, two a box (extents multiples of 64)
     int32_t *status;
@@ -62,12 +63,13 @@ struct GemmParams {
 
 // Tensor maps. w: weights [E][N][K]; rows: the rows that are N (forward, dgrad)
 // in boxes of 16, 32, 64, 96 and 128 rows, so that a tile's are one load; rows[0]
-// of wgrad: the rows that are M; dy: wgrad's other operand; out: the result, in
-// boxes of 32 M and 32 (16-bit) or 16 (fp32) columns.
+// of wgrad: the rows that are M; dy: wgrad's other operand; out, base: the
+// result and wgrad's sum so far, in boxes of 32 M and 32 (16-bit) or 16 (fp32)
+// columns.
 constexpr int kBoxes = 5;
 __host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 16 : 32 * i; }
 struct GemmMaps {
-    CUtensorMap w, rows[kBoxes], dy, out;
+    CUtensorMap w, rows[kBoxes], dy, out, base;
 };
 
 // One expert that has tiles: its first tile, rows and id.
@@ -76,7 +78,7 @@ struct Entry {
 };
 
 struct GemmSmem {
-    uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages], tfull[2], tempty[2];
+    uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages], tfull[2], tempty[2], based[kEpiWarps];
     uint32_t tmem_base;
     int abort, entries;
     int warp_tiles[32], warp_entries[32];
@@ -92,9 +94,12 @@ struct Cfg {
     static constexpr int kBRows = TN / CG;  // of B a CTA holds
     static constexpr int kA = kTileM * 128, kB = kBRows * 128, kStage = kA + kB;
     // shared memory: the ring, the epilogue's turning space, the table of E + 1 entries
-    static constexpr size_t fixed(int E) { return kEpiWarps * kTurn + (size_t(E) + 1) * sizeof(Entry) + 1024; }
-    static constexpr int stages(int E) {
-        const size_t fit = (232448 - 1024 - fixed(E)) / kStage;  // 1 KB: GemmSmem
+    // (twice with a sum to read)
+    static constexpr size_t fixed(int E, int read_base) {
+        return kEpiWarps * kTurn * (1 + read_base) + (size_t(E) + 1) * sizeof(Entry) + 1024;
+    }
+    static constexpr int stages(int E, int read_base) {
+        const size_t fit = (232448 - 1024 - fixed(E, read_base)) / kStage;  // 1 KB: GemmSmem
         return fit < size_t(kMaxStages) ? int(fit) : kMaxStages;
     }
     // Tensor memory: two buffers, so that the epilogue of one tile runs beside the
@@ -103,7 +108,7 @@ struct Cfg {
     // instead of round, an error that grows with the length of a chain. Narrow
     // tiles have room for four in each buffer; wide ones take both buffers.
     static constexpr int kAccs = CG == 1 ? 4 : 2, kBuf = CG == 1 ? kAccs * TN : TN, kCols = 2 * kBuf;
-    static_assert(stages(kMaxE) >= 4 && sizeof(GemmSmem) <= 1024 && kCols >= 32 && kCols <= 512, "tile does not fit");
+    static_assert(stages(kMaxE, PASS == kWgrad) >= 4 && sizeof(GemmSmem) <= 1024 && kCols >= 32 && kCols <= 512, "tile does not fit");
 };
 
 __device__ __forceinline__ void stop(GemmSmem &s, int32_t *status) {
@@ -527,49 +532,55 @@ __device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, 
 // Epilogue warps: lane quadrant warp % 4 of tensor memory, every second 32
 // columns. Results pass through this warp's 2 KB of shared memory and leave as
 // TMA boxes of 32 M and 32 columns (fp32: 16), those of a tile's ragged end as
-// plain stores: a box would reach the next expert's rows.
-
-// 32 x 32 accumulators (lanes M, columns), as fragments v of two 16-lane
-// halves, to [column][32] in 16 bits: packed along the columns, turned by the
-// transposing matrix store, 16-byte chunks in the 64-byte swizzle.
-template <typename O>
-__device__ __forceinline__ void turn16(const uint32_t (&v)[2][16], uint32_t turn) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float lo = __uint_as_float(v[j >> 1][4 * i + 2 * (j & 1)]);
-            const float hi = __uint_as_float(v[j >> 1][4 * i + 2 * (j & 1) + 1]);
-            const O pair[2] = {from_f32<O>(lo), from_f32<O>(hi)};
-            w[j] = *reinterpret_cast<const uint32_t *>(pair);
+// plain stores: a box would reach the next expert's rows. An fp32 sum so far
+// that is in place is added to by the reduction of the boxes, where they land;
+// another one, and one of 16 bits (which is rounded only after the addition),
+// comes as the same boxes into 2 KB more, one box ahead of its use.
+struct Out {
+    const CUtensorMap *out, *base;
+    uint64_t *based;      // this warp's barrier for boxes of the sum so far
+    uint32_t turn, sum;   // the two 2 KB
+    uint32_t phase;
+    // Lane 0: ask for the box of the sum at column c of tile t.
+    __device__ __forceinline__ void want(const Tile &t, int m1, int c) {
+        if ((threadIdx.x & 31) == 0) {
+            tc::mbar_arrive_expect_tx(based, kTurn);
+            tc::tma_load_3d_at(sum, base, m1, t.c0 + c, t.e, tc::smem_u32(based));
         }
-        const int n = 8 * i + (lane & 7), ch = lane >> 3;
-        tc::stmatrix_x4_trans(turn + n * 64 + ((ch ^ ((n >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
     }
-}
-// Columns below `cols` of them to memory, 16 bytes a lane.
-template <typename O>
-__device__ __forceinline__ void store16(uint32_t turn, O *out, int64_t pitch, int cols, int m_left) {
-    const int lane = threadIdx.x & 31, ch = lane & 3, n0 = lane >> 2;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // columns 8 apart have the same swizzle
-        uint4 r;
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                     : "r"(turn + n0 * 64 + ((ch ^ ((n0 >> 1) & 3)) << 4) + i * 512));
-        if (8 * ch < m_left && n0 + 8 * i < cols) *reinterpret_cast<uint4 *>(out + (n0 + 8 * i) * pitch + 8 * ch) = r;
+    __device__ __forceinline__ bool got() {
+        const bool ok = tc::mbar_wait_warp(based, phase, kWaitNs);
+        phase ^= 1;
+        return ok;
     }
-}
+    // The buffer's last box has been read by its store.
+    __device__ __forceinline__ void free_turn() {
+        if ((threadIdx.x & 31) == 0) tc::bulk_wait_read<0>();
+        __syncwarp();
+    }
+    // The buffer, written by the whole warp, as a box.
+    __device__ __forceinline__ void store(int m1, int row, int slab, bool add) {
+        tc::fence_proxy_async();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            if (add) tc::tma_add_3d(out, m1, row, slab, turn);
+            else tc::tma_store_3d(out, m1, row, slab, turn);
+            tc::bulk_commit();
+        }
+    }
+};
 
-// 16-bit results. The next 32 columns are on their way while these are stored.
+// 16-bit results. 32 x 32 accumulators (lanes M, columns), as fragments of two
+// 16-lane halves, are packed along the columns and turned by the transposing
+// matrix store into [column][32], 16-byte chunks in the 64-byte swizzle. The
+// next 32 columns are on their way while these are stored.
 template <typename C, typename O>
-__device__ __forceinline__ void store_tile16(const GemmParams &p, const CUtensorMap &map, const Tile &t, bool sums,
-                                             uint32_t td, uint32_t turn, int half, int m1) {
+__device__ __forceinline__ bool store_tile16(const GemmParams &p, Out &to, const Tile &t, bool sums, uint32_t td,
+                                             int half, int m1) {
     const int lane = threadIdx.x & 31;
-    const int64_t row0 = C::PASS == kWgrad ? int64_t(t.e) * p.N + t.c0 : int64_t(t.c0);
-    O *o = static_cast<O *>(p.out) + row0 * p.M + m1;
+    const uint32_t at = (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);  // + 512 i: column 8 i + lane % 8
+    const bool add = C::PASS == kWgrad && p.read_base;
+    bool ok = true;
     uint32_t v[2][2][16];
     auto fetch = [&](int c, uint32_t(&f)[2][16]) {
         if (sums && c < t.n) {
@@ -577,20 +588,48 @@ __device__ __forceinline__ void store_tile16(const GemmParams &p, const CUtensor
             tc::tmem_ld16x256_x4_nowait(td + c + (16u << 16), f[1]);
         }
     };
-    auto store = [&](int c, const uint32_t(&f)[2][16]) {
-        if (lane == 0) tc::bulk_wait_read<0>();
-        __syncwarp();  // the columns before have left the buffer
-        turn16<O>(f, turn);
-        if (C::PASS == kWgrad || c + 32 <= t.n) {
-            tc::fence_proxy_async();
+    auto put = [&](int c, const uint32_t(&f)[2][16]) {
+        uint32_t old[4][4];
+        if (add) {
+            ok = to.got() && ok;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc::ldmatrix_x4_trans(to.sum + at + 512 * i, old[i]);
             __syncwarp();
-            if (lane == 0 && m1 < p.M) {
-                tc::tma_store_3d(&map, m1, t.c0 + c, C::PASS == kWgrad ? t.e : 0, turn);
-                tc::bulk_commit();
+            if (c + 64 < t.n) to.want(t, m1, c + 64);
+        }
+        to.free_turn();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float lo = __uint_as_float(f[j >> 1][4 * i + 2 * (j & 1)]);
+                float hi = __uint_as_float(f[j >> 1][4 * i + 2 * (j & 1) + 1]);
+                if (add) {
+                    const O *o = reinterpret_cast<const O *>(&old[i][j]);
+                    lo += to_f32(o[0]);
+                    hi += to_f32(o[1]);
+                }
+                const O pair[2] = {from_f32<O>(lo), from_f32<O>(hi)};
+                w[j] = *reinterpret_cast<const uint32_t *>(pair);
             }
+            tc::stmatrix_x4_trans(to.turn + at + 512 * i, w[0], w[1], w[2], w[3]);
+        }
+        if (C::PASS == kWgrad || c + 32 <= t.n) {
+            to.store(m1, t.c0 + c, C::PASS == kWgrad ? t.e : 0, false);
         } else {
             __syncwarp();
-            store16<O>(turn, o + int64_t(c) * p.M, p.M, t.n - c, p.M - m1);
+            const int ch = lane & 3, n0 = lane >> 2;  // 16 bytes a lane; columns 8 apart have the same swizzle
+            O *o = static_cast<O *>(p.out) + int64_t(t.c0 + c + n0) * p.M + m1 + 8 * ch;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint4 r;
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                             : "r"(to.turn + n0 * 64 + ((ch ^ ((n0 >> 1) & 3)) << 4) + i * 512));
+                if (m1 + 8 * ch < p.M && c + n0 + 8 * i < t.n)
+                    *reinterpret_cast<uint4 *>(o + int64_t(8 * i) * p.M) = r;
+            }
         }
     };
     if (!sums)
@@ -600,18 +639,24 @@ __device__ __forceinline__ void store_tile16(const GemmParams &p, const CUtensor
     for (int c = 32 * half; c < t.n; c += 128) {
         tc::tmem_ld_wait();
         fetch(c + 64, v[1]);
-        store(c, v[0]);
+        put(c, v[0]);
         if (c + 64 < t.n) {
             tc::tmem_ld_wait();
             fetch(c + 128, v[0]);
-            store(c + 64, v[1]);
+            put(c + 64, v[1]);
         }
     }
+    return ok;
 }
 
-// 32 columns of fp32, the sum of `accs` accumulators.
+// 32 columns of fp32, the sum of `accs` accumulators (none: zeros).
 template <typename C>
 __device__ __forceinline__ void fetch32(uint32_t td, int accs, uint32_t (&v)[32]) {
+    if (accs == 0) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0u;
+        return;
+    }
     tc::tmem_ld32_nowait(td, v);
     tc::tmem_ld_wait();
     for (int a = 1; a < accs; ++a) {
@@ -623,39 +668,40 @@ __device__ __forceinline__ void fetch32(uint32_t td, int accs, uint32_t (&v)[32]
     }
 }
 
-// fp32 results, 16 columns at a time; into a sum that is in place by the
-// reduction of the boxes, which adds them where they land.
+// fp32 results, [column][32], 16 columns at a time.
 template <typename C>
-__device__ __forceinline__ void store_tile32(const GemmParams &p, const CUtensorMap &map, const Tile &t, int accs,
-                                             uint32_t td, uint32_t turn, int half, int m1) {
+__device__ __forceinline__ bool store_tile32(const GemmParams &p, Out &to, const Tile &t, int accs, uint32_t td,
+                                             int half, int m1) {
     const int lane = threadIdx.x & 31, m = m1 + lane;
-    const bool add = C::PASS == kWgrad && p.base;
-    float *o = static_cast<float *>(p.out) + (C::PASS == kWgrad ? int64_t(t.e) * p.N + t.c0 : int64_t(t.c0)) * p.M + m;
+    const bool add = C::PASS == kWgrad && p.read_base;
+    bool ok = true;
+    float *o = static_cast<float *>(p.out) + int64_t(t.c0) * p.M + m;
     for (int c = 32 * half; c < t.n; c += 64) {
         uint32_t v[32];
-        if (accs) {
-            fetch32<C>(td + c, accs, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
-        }
+        fetch32<C>(td + c, accs, v);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int c1 = c + 16 * h;
             if (c1 >= t.n) break;
-            if (C::PASS == kWgrad || c1 + 16 <= t.n) {
-                if (lane == 0) tc::bulk_wait_read<0>();
+            if (add) {
+                ok = to.got() && ok;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float old;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(old) : "r"(to.sum + i * 128 + lane * 4));
+                    v[16 * h + i] = __float_as_uint(__uint_as_float(v[16 * h + i]) + old);
+                }
                 __syncwarp();
+                const int next = h ? c + 64 : c1 + 16 < t.n ? c1 + 16 : c + 64;
+                if (next < t.n) to.want(t, m1, next);
+            }
+            if (C::PASS == kWgrad || c1 + 16 <= t.n) {
+                to.free_turn();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(turn + i * 128 + lane * 4), "r"(v[16 * h + i]) : "memory");
-                tc::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0 && m1 < p.M) {
-                    if (add) tc::tma_add_3d(&map, m1, t.c0 + c1, t.e, turn);
-                    else tc::tma_store_3d(&map, m1, t.c0 + c1, C::PASS == kWgrad ? t.e : 0, turn);
-                    tc::bulk_commit();
-                }
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to.turn + i * 128 + lane * 4), "r"(v[16 * h + i])
+                                 : "memory");
+                to.store(m1, t.c0 + c1, C::PASS == kWgrad ? t.e : 0, C::PASS == kWgrad && p.base && !add);
             } else if (m < p.M) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -663,101 +709,40 @@ __device__ __forceinline__ void store_tile32(const GemmParams &p, const CUtensor
             }
         }
     }
+    return ok;
 }
 
-// wgrad onto a sum that is elsewhere (or in 16 bits, which are rounded only
-// after the addition): read and added here. fp32: a column's 32 consecutive
-// values at a time; 16 bits: two columns at once (lane pairs swap values so that
-// each lane holds two neighbours of one column). The first 32 columns of the
-// sum are read while the products still run, the others 32 ahead of their use.
 template <typename C, typename O>
-struct AddTile {
-    static constexpr bool kWide = sizeof(O) == 4;
-    static constexpr int kVals = kWide ? 32 : 16;  // 32-bit words a lane stores of 32 columns
-    uint32_t old[kVals];
-    int64_t at0;
-    bool in;
-    int odd;
-    __device__ __forceinline__ void read(const GemmParams &p, const Tile &t, int c) {
-        const O *b = static_cast<const O *>(p.base) + at0 + int64_t(c) * p.M;
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) {
-            const int col = kWide ? i : 2 * i;
-            old[i] = in && c + col + (kWide ? 0 : odd) < t.n
-                         ? *reinterpret_cast<const uint32_t *>(b + int64_t(col) * p.M) : 0u;
-        }
-    }
-    __device__ __forceinline__ void begin(const GemmParams &p, const Tile &t, int half, int m1) {
-        const int m = m1 + (threadIdx.x & 31);
-        odd = threadIdx.x & 1;
-        in = m < p.M;
-        const int64_t row0 = int64_t(t.e) * p.N + t.c0;
-        // word i of 32 columns from c: fp32 column c + i; 16 bits column c + 2 i + odd, elements m & ~1 and next
-        at0 = kWide ? row0 * p.M + m : (row0 + odd) * p.M + (m & ~1);
-        if (32 * half < t.n) read(p, t, 32 * half);
-    }
-    __device__ __forceinline__ void store(const GemmParams &p, const Tile &t, int accs, uint32_t td, int half) {
-        for (int c = 32 * half; c < t.n; c += 64) {
-            uint32_t v[32], word[kVals];
-            if (accs) {
-                fetch32<C>(td + c, accs, v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < kVals; ++i) {
-                if (kWide) {
-                    word[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(old[i]));
-                } else {
-                    const uint32_t a = v[(2 * i) & 31], b = v[(2 * i + 1) & 31];
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                    const O *o = reinterpret_cast<const O *>(&old[i]);
-                    const O pair[2] = {from_f32<O>(__uint_as_float(odd ? got : a) + to_f32(o[0])),
-                                       from_f32<O>(__uint_as_float(odd ? b : got) + to_f32(o[1]))};
-                    word[i] = *reinterpret_cast<const uint32_t *>(pair);
-                }
-            }
-            if (c + 64 < t.n) read(p, t, c + 64);
-            O *o = static_cast<O *>(p.out) + at0 + int64_t(c) * p.M;
-#pragma unroll
-            for (int i = 0; i < kVals; ++i) {
-                const int col = kWide ? i : 2 * i;
-                if (in && c + col + (kWide ? 0 : odd) < t.n)
-                    *reinterpret_cast<uint32_t *>(o + int64_t(col) * p.M) = word[i];
-            }
-        }
-    }
-};
-
-template <typename C, typename O>
-__device__ void store_tiles(const GemmParams &p, GemmSmem &s, const CUtensorMap &map, unsigned char *dyn, Walk<C> walk,
+__device__ void store_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &maps, unsigned char *dyn, Walk<C> walk,
                             int total, uint32_t tmem) {
     const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = threadIdx.x & 31;
     const int q = (warp + kEpiWarp0) & 3, half = warp >> 2;
     const uint32_t turn = tc::smem_u32(dyn) + p.stages * C::kStage + warp * kTurn;
-    const bool read_base = C::PASS == kWgrad && p.base && (sizeof(O) == 2 || p.base != p.out);
+    Out to = {&maps.out, &maps.base, &s.based[warp], turn, turn + kEpiWarps * kTurn, 0};
     int count = 0;
     for (int tau = blockIdx.x / C::CG; tau < total && !s.abort; tau += gridDim.x / C::CG) {
         const Tile t = walk.tile(p, tau);
         const int KS = stages_of<C>(p, t), accs = p.split ? min(C::kAccs, KS) : min(1, KS);  // 0: no sums
         uint32_t phase;
         const int m1 = t.m0 + 32 * q, buf = buffer_of<C>(p, count, phase);
-        AddTile<C, O> sum;
-        if (read_base) sum.begin(p, t, half, m1);
+        const bool any = m1 < p.M && 32 * half < t.n;  // of this warp's values lie in the result
+        if (C::PASS == kWgrad && p.read_base && any) to.want(t, m1, 32 * half);
+        bool ok = true;
         if (accs) {
-            if (!tc::mbar_wait(&s.tfull[buf], phase, kWaitNs)) {
-                stop(s, p.status);
-                break;
-            }
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.tfull[buf], phase, kWaitNs));
             tc::fence_after();
             ++count;
         }
-        __syncwarp();
         const uint32_t td = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * C::kBuf);
-        if (read_base) sum.store(p, t, accs, td, half);
-        else if constexpr (sizeof(O) == 2) store_tile16<C, O>(p, map, t, accs > 0, td, turn, half, m1);
-        else store_tile32<C>(p, map, t, accs, td, turn, half, m1);
+        if (ok && any) {
+            if constexpr (sizeof(O) == 2) ok = store_tile16<C, O>(p, to, t, accs > 0, td, half, m1);
+            else ok = store_tile32<C>(p, to, t, accs, td, half, m1);
+        }
+        if (!ok) {  // no box may land after this CTA's shared memory has another owner
+            stop(s, p.status);
+            if (C::PASS == kWgrad && p.read_base && any) to.got();
+            break;
+        }
         if (accs) {
             tc::fence_before();
             __syncwarp();
@@ -790,6 +775,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             tc::mbar_init(&s.tfull[i], 1);
             tc::mbar_init(&s.tempty[i], C::CG * kEpiWarps);
         }
+        for (int i = 0; i < kEpiWarps; ++i) tc::mbar_init(&s.based[i], 1);
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -797,7 +783,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (C::CG == 2) tc::tmem_alloc_pair(&s.tmem_base, C::kCols);
         else tc::tmem_alloc(&s.tmem_base, C::kCols);
     }
-    Entry *table = reinterpret_cast<Entry *>(dyn + p.stages * C::kStage + kEpiWarps * kTurn);
+    Entry *table = reinterpret_cast<Entry *>(dyn + p.stages * C::kStage + kEpiWarps * kTurn * (1 + p.read_base));
     const int total = build_table<C>(p, s, table, MT);
     tc::fence_before();
     if (C::CG == 2) tc::cluster_sync();  // both CTAs' barriers are set up
@@ -815,11 +801,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             else gather_tiles<C>(p, s, dyn, walk, total);
         }
     } else if (p.out_fp32) {
-        store_tiles<C, float>(p, s, maps.out, dyn, walk, total, tmem);
+        store_tiles<C, float>(p, s, maps, dyn, walk, total, tmem);
     } else if (p.bf16) {
-        store_tiles<C, __nv_bfloat16>(p, s, maps.out, dyn, walk, total, tmem);
+        store_tiles<C, __nv_bfloat16>(p, s, maps, dyn, walk, total, tmem);
     } else {
-        store_tiles<C, __half>(p, s, maps.out, dyn, walk, total, tmem);
+        store_tiles<C, __half>(p, s, maps, dyn, walk, total, tmem);
     }
     __syncwarp();
     tc::fence_before();
@@ -898,8 +884,8 @@ bool map_blocks(CUtensorMap *m, bool bf16, const void *base, int64_t inner, int6
 
 template <typename C>
 moe_status launch(GemmParams &p, const GemmMaps &maps, int64_t most_tiles, int sms, cudaStream_t stream) {
-    p.stages = C::stages(p.E);
-    const size_t smem = p.stages * C::kStage + C::fixed(p.E);
+    p.stages = C::stages(p.E, p.read_base);
+    const size_t smem = p.stages * C::kStage + C::fixed(p.E, p.read_base);
     if (cudaFuncSetAttribute(expert_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
         cudaSuccess) {
         cudaGetLastError();
@@ -945,6 +931,8 @@ moe_status run_gemm(int pass, GemmParams &p, const void *w, int N, int K, cudaSt
     p.blocks2 = pass == kWgrad ? N % 64 == 0 && K % 64 == 0 : pass == kDgrad && K % 64 == 0;
     bool ok = pass == kWgrad ? map_out(&maps.out, bf, p.out_fp32, p.out, K, N, p.E)
                              : map_out(&maps.out, bf, p.out_fp32, p.out, p.M, p.P, 1);
+    p.read_base = p.base && (!p.out_fp32 || p.base != p.out);
+    if (p.read_base) ok = ok && map_out(&maps.base, bf, p.out_fp32, p.base, K, N, p.E);
     if (p.P > 0) {  // an empty batch (wgrad) has no rows to describe, and loads none
         if (pass == kForward)
             ok = ok && map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 128, 1, 1});
@@ -998,7 +986,7 @@ MOE_API moe_status moe_expert_gemm(const void *a, const void *W, int dtype, int 
     if (st != MOE_OK || T == 0) return st;
     if (!a || !W || !offsets || !out || !aligned16(a) || !aligned16(W) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), nullptr, nullptr, out, sorted_tok ? T : T * k,
-                    T * k, E, N, K, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, dev_status};
+                    T * k, E, N, K, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, 0, dev_status};
     return run_gemm(kForward, p, W, N, K, as_cuda(stream));
 }
 
@@ -1009,7 +997,7 @@ MOE_API moe_status moe_expert_gemm_dgrad(const void *dy, const void *W, int dtyp
     if (st != MOE_OK || T == 0) return st;
     if (!dy || !W || !offsets || !da || !aligned16(dy) || !aligned16(W) || !aligned16(da)) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, nullptr, static_cast<const uint16_t *>(dy), nullptr, nullptr, da,
-                    T * k, T * k, E, K, N, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, dev_status};
+                    T * k, T * k, E, K, N, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, 0, dev_status};
     return run_gemm(kDgrad, p, W, N, K, as_cuda(stream));
 }
 
@@ -1022,6 +1010,6 @@ MOE_API moe_status moe_expert_gemm_wgrad(const void *dy, const void *a, int dtyp
     if (T > 0 && (!dy || !a || !aligned16(dy) || !aligned16(a))) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), static_cast<const uint16_t *>(dy), base, dW,
                     sorted_tok ? T : T * k, T * k, E, K, 0, N, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0,
-                    dev_status};
+                    0, dev_status};
     return run_gemm(kWgrad, p, nullptr, N, K, as_cuda(stream));
 }
