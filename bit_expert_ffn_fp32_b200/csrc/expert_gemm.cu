@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "tc05.cuh"
@@ -540,26 +541,25 @@ struct Out {
     const CUtensorMap *out, *base;
     uint64_t *based;      // this warp's barrier for boxes of the sum so far
     uint32_t turn, sum;   // the two 2 KB
-    uint32_t phase;
     // Lane 0: ask for the box of the sum at column c of tile t.
-    __device__ __forceinline__ void want(const Tile &t, int m1, int c) {
+    __device__ __forceinline__ void want(const Tile &t, int m1, int c) const {
         if ((threadIdx.x & 31) == 0) {
             tc::mbar_arrive_expect_tx(based, kTurn);
             tc::tma_load_3d_at(sum, base, m1, t.c0 + c, t.e, tc::smem_u32(based));
         }
     }
-    __device__ __forceinline__ bool got() {
+    __device__ __forceinline__ bool got(uint32_t &phase) const {
         const bool ok = tc::mbar_wait_warp(based, phase, kWaitNs);
         phase ^= 1;
         return ok;
     }
     // The buffer's last box has been read by its store.
-    __device__ __forceinline__ void free_turn() {
+    __device__ __forceinline__ void free_turn() const {
         if ((threadIdx.x & 31) == 0) tc::bulk_wait_read<0>();
         __syncwarp();
     }
     // The buffer, written by the whole warp, as a box.
-    __device__ __forceinline__ void store(int m1, int row, int slab, bool add) {
+    __device__ __forceinline__ void store(int m1, int row, int slab, bool add) const {
         tc::fence_proxy_async();
         __syncwarp();
         if ((threadIdx.x & 31) == 0) {
@@ -574,12 +574,11 @@ struct Out {
 // 16-lane halves, are packed along the columns and turned by the transposing
 // matrix store into [column][32], 16-byte chunks in the 64-byte swizzle. The
 // next 32 columns are on their way while these are stored.
-template <typename C, typename O>
-__device__ __forceinline__ bool store_tile16(const GemmParams &p, Out &to, const Tile &t, bool sums, uint32_t td,
-                                             int half, int m1) {
+template <typename C, typename O, bool ADD>
+__device__ __forceinline__ bool store_tile16(const GemmParams &p, const Out &to, uint32_t &based, const Tile &t,
+                                             bool sums, uint32_t td, int half, int m1) {
     const int lane = threadIdx.x & 31;
     const uint32_t at = (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);  // + 512 i: column 8 i + lane % 8
-    const bool add = C::PASS == kWgrad && p.read_base;
     bool ok = true;
     uint32_t v[2][2][16];
     auto fetch = [&](int c, uint32_t(&f)[2][16]) {
@@ -590,8 +589,8 @@ __device__ __forceinline__ bool store_tile16(const GemmParams &p, Out &to, const
     };
     auto put = [&](int c, const uint32_t(&f)[2][16]) {
         uint32_t old[4][4];
-        if (add) {
-            ok = to.got() && ok;
+        if (ADD) {
+            ok = to.got(based) && ok;
 #pragma unroll
             for (int i = 0; i < 4; ++i) tc::ldmatrix_x4_trans(to.sum + at + 512 * i, old[i]);
             __syncwarp();
@@ -605,7 +604,7 @@ __device__ __forceinline__ bool store_tile16(const GemmParams &p, Out &to, const
             for (int j = 0; j < 4; ++j) {
                 float lo = __uint_as_float(f[j >> 1][4 * i + 2 * (j & 1)]);
                 float hi = __uint_as_float(f[j >> 1][4 * i + 2 * (j & 1) + 1]);
-                if (add) {
+                if (ADD) {
                     const O *o = reinterpret_cast<const O *>(&old[i][j]);
                     lo += to_f32(o[0]);
                     hi += to_f32(o[1]);
@@ -635,6 +634,14 @@ __device__ __forceinline__ bool store_tile16(const GemmParams &p, Out &to, const
     if (!sums)
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[0][0][i] = v[0][1][i] = v[1][0][i] = v[1][1][i] = 0u;
+    if constexpr (C::PICK == 2) {  // 640 threads have no registers for it
+        for (int c = 32 * half; c < t.n; c += 64) {
+            fetch(c, v[0]);
+            tc::tmem_ld_wait();
+            put(c, v[0]);
+        }
+        return ok;
+    }
     fetch(32 * half, v[0]);
     for (int c = 32 * half; c < t.n; c += 128) {
         tc::tmem_ld_wait();
@@ -669,11 +676,10 @@ __device__ __forceinline__ void fetch32(uint32_t td, int accs, uint32_t (&v)[32]
 }
 
 // fp32 results, [column][32], 16 columns at a time.
-template <typename C>
-__device__ __forceinline__ bool store_tile32(const GemmParams &p, Out &to, const Tile &t, int accs, uint32_t td,
-                                             int half, int m1) {
+template <typename C, bool ADD>
+__device__ __forceinline__ bool store_tile32(const GemmParams &p, const Out &to, uint32_t &based, const Tile &t,
+                                             int accs, uint32_t td, int half, int m1) {
     const int lane = threadIdx.x & 31, m = m1 + lane;
-    const bool add = C::PASS == kWgrad && p.read_base;
     bool ok = true;
     float *o = static_cast<float *>(p.out) + int64_t(t.c0) * p.M + m;
     for (int c = 32 * half; c < t.n; c += 64) {
@@ -683,8 +689,8 @@ __device__ __forceinline__ bool store_tile32(const GemmParams &p, Out &to, const
         for (int h = 0; h < 2; ++h) {
             const int c1 = c + 16 * h;
             if (c1 >= t.n) break;
-            if (add) {
-                ok = to.got() && ok;
+            if (ADD) {
+                ok = to.got(based) && ok;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float old;
@@ -701,7 +707,7 @@ __device__ __forceinline__ bool store_tile32(const GemmParams &p, Out &to, const
                 for (int i = 0; i < 16; ++i)
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(to.turn + i * 128 + lane * 4), "r"(v[16 * h + i])
                                  : "memory");
-                to.store(m1, t.c0 + c1, C::PASS == kWgrad ? t.e : 0, C::PASS == kWgrad && p.base && !add);
+                to.store(m1, t.c0 + c1, C::PASS == kWgrad ? t.e : 0, C::PASS == kWgrad && p.base && !ADD);
             } else if (m < p.M) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -712,13 +718,14 @@ __device__ __forceinline__ bool store_tile32(const GemmParams &p, Out &to, const
     return ok;
 }
 
-template <typename C, typename O>
+template <typename C, typename O, bool ADD>
 __device__ void store_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &maps, unsigned char *dyn, Walk<C> walk,
                             int total, uint32_t tmem) {
     const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = threadIdx.x & 31;
     const int q = (warp + kEpiWarp0) & 3, half = warp >> 2;
     const uint32_t turn = tc::smem_u32(dyn) + p.stages * C::kStage + warp * kTurn;
-    Out to = {&maps.out, &maps.base, &s.based[warp], turn, turn + kEpiWarps * kTurn, 0};
+    const Out to = {&maps.out, &maps.base, &s.based[warp], turn, turn + kEpiWarps * kTurn};
+    uint32_t based = 0;
     int count = 0;
     for (int tau = blockIdx.x / C::CG; tau < total && !s.abort; tau += gridDim.x / C::CG) {
         const Tile t = walk.tile(p, tau);
@@ -726,7 +733,7 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &ma
         uint32_t phase;
         const int m1 = t.m0 + 32 * q, buf = buffer_of<C>(p, count, phase);
         const bool any = m1 < p.M && 32 * half < t.n;  // of this warp's values lie in the result
-        if (C::PASS == kWgrad && p.read_base && any) to.want(t, m1, 32 * half);
+        if (ADD && any) to.want(t, m1, 32 * half);
         bool ok = true;
         if (accs) {
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.tfull[buf], phase, kWaitNs));
@@ -735,12 +742,12 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &ma
         }
         const uint32_t td = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * C::kBuf);
         if (ok && any) {
-            if constexpr (sizeof(O) == 2) ok = store_tile16<C, O>(p, to, t, accs > 0, td, half, m1);
-            else ok = store_tile32<C>(p, to, t, accs, td, half, m1);
+            if constexpr (sizeof(O) == 2) ok = store_tile16<C, O, ADD>(p, to, based, t, accs > 0, td, half, m1);
+            else ok = store_tile32<C, ADD>(p, to, based, t, accs, td, half, m1);
         }
         if (!ok) {  // no box may land after this CTA's shared memory has another owner
             stop(s, p.status);
-            if (C::PASS == kWgrad && p.read_base && any) to.got();
+            if (ADD && any) to.got(based);
             break;
         }
         if (accs) {
@@ -800,12 +807,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             if (warp == C::kRelayWarp) relay_stages<C>(p, s, walk, total);
             else gather_tiles<C>(p, s, dyn, walk, total);
         }
-    } else if (p.out_fp32) {
-        store_tiles<C, float>(p, s, maps, dyn, walk, total, tmem);
-    } else if (p.bf16) {
-        store_tiles<C, __nv_bfloat16>(p, s, maps, dyn, walk, total, tmem);
     } else {
-        store_tiles<C, __half>(p, s, maps, dyn, walk, total, tmem);
+        auto store = [&](auto add) {
+            constexpr bool kAdd = decltype(add)::value;
+            if (p.out_fp32) store_tiles<C, float, kAdd>(p, s, maps, dyn, walk, total, tmem);
+            else if (p.bf16) store_tiles<C, __nv_bfloat16, kAdd>(p, s, maps, dyn, walk, total, tmem);
+            else store_tiles<C, __half, kAdd>(p, s, maps, dyn, walk, total, tmem);
+        };
+        if (C::PASS == kWgrad && p.read_base) store(std::integral_constant<bool, C::PASS == kWgrad>());
+        else store(std::false_type());
     }
     __syncwarp();
     tc::fence_before();
