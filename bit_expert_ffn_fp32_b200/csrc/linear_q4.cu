@@ -228,8 +228,9 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
         const int quads = min(p.chunk * (kStep / 32), p.K / 32 - c0 * (kStep / 32)), cgroups = quads * 32 / G;  // of 32 k
         const int quads4 = (quads + 3) & ~3;  // of whole 128 k, so that the four of one stay together
         if (c0) __syncthreads();
-        for (int i = threadIdx.x; i < ((tiles * quads4 << ts) + 31 & ~31); i += 32 * kWarps) {
-            // one token's 32 k: lanes of one token are TS apart, so a group's sum is a shuffle away
+        // one token's 32 k: lanes of one token are TS apart, so the sums and the largest of 128 k are a shuffle away
+        const int all = (tiles * quads4 << ts) + 31 & ~31;
+        auto load = [&](int i, uint4(&v)[4]) {
             const int tq = i >> ts, nb = tq / quads4, quad = tq - nb * quads4, tok = 8 * nb + (i & (TS - 1));
             int row = -1;
             if (nb < tiles && quad < quads && tok < n) {
@@ -242,7 +243,6 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
                     }
                 }
             }
-            uint4 v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
             if (row >= 0) {
@@ -251,6 +251,15 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] = __ldg(from + k);
             }
+        };
+        uint4 next[4];
+        if (int(threadIdx.x) < all) load(threadIdx.x, next);
+        for (int i = threadIdx.x; i < all; i += 32 * kWarps) {
+            const int tq = i >> ts, nb = tq / quads4, quad = tq - nb * quads4;
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = next[k];
+            if (i + 32 * kWarps < all) load(i + 32 * kWarps, next);  // on its way while these are scaled
             // the power of two of these 128 k: 14 less the exponent of their largest
             float x[4][8], most = 0.f;
 #pragma unroll
@@ -513,24 +522,29 @@ moe_status run_q4(const moe_q4weights *W, Q4Params &p, const void *x, int dtype,
     p.swiglu = act == MOE_ACT_SWIGLU;
     p.scales_in_words = W->K % kStep == 0 && reinterpret_cast<uintptr_t>(W->scale) % 16 == 0 &&
                         reinterpret_cast<uintptr_t>(W->min) % 16 == 0;
-    // Token tiles: as many as the rows a matrix has on average (at most T) fill.
-    const int rows = std::min(p.T, 2 * ((p.P + experts - 1) / experts));
-    const int nb = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    // Token tiles: as many as a third more rows than a matrix has on average (at
+    // most T) fill; two of four, if then 8 warps can share 16 rows in one turn of
+    // an SM each. (64 experts with 5.8 rows: 48 us with one tile, 84 with two; 512
+    // x 8192, 20 tokens: 31 us with two, 43 with four.)
+    const int rows = int(std::min<int64_t>(p.T, (4 * int64_t(p.P) + 3 * experts - 1) / (3 * experts)));
+    const int64_t units = int64_t(p.N / 32) * experts;
+    const int nb = rows <= 8 ? 1 : rows <= 16 || (!p.swiglu && 2 * units <= 148) ? 2 : 4;
     p.ts_log2 = nb > 1 || p.T > 4 ? 3 : p.T > 2 ? 2 : p.T > 1 ? 1 : 0;
     // Warps that share rows: as many as leave all blocks running at once (two an
-    // SM), up to 8 (4 with four token tiles, whose x would not fit); then 16 rows
-    // a warp. Where the blocks take several turns anyway, pairs of warps, unless
-    // k is too short to split. Measured (warps a row: us): gate and up rows of
-    // one token 1: 13.0, 2: 8.8, 4: 8.2, 8: 10.7 (480 blocks); 8192 x 8192, one
-    // token 1: 32, 2: 19, 4: 12.8, 8: 12.1; gate and up rows of 37 tokens 1: 91,
-    // 2: 79, 4: 89; down rows (3 steps of k) of four tokens 1: 17, 2: 20, 4: 24.
-    constexpr int64_t kSlots = 148 * 2 * kWarps;
+    // SM; one, where staging the x of several tokens weighs more than the codes),
+    // up to 8 (4 with four token tiles, whose x would not fit); then 16 rows a
+    // warp. Where the blocks take several turns anyway, pairs of warps, unless k
+    // is too short to split. Measured (warps a row: us): gate and up rows of one
+    // token 1: 13.0, 2: 8.8, 4: 8.2, 8: 10.7 (480 blocks); 8192 x 8192, one token
+    // 1: 32, 2: 19, 4: 12.8, 8: 12.1 (256 blocks), five tokens 4: 22, 8: 28; gate
+    // and up rows of 37 tokens 1: 91, 2: 79, 4: 89; down rows (3 steps of k) of
+    // four tokens 1: 17, 2: 20, 4: 24.
+    const int64_t slots = 148 * kWarps * (rows > 2 ? 1 : 2);
     const int steps = (p.K + kStep - 1) / kStep, most = nb == 4 ? 2 : 3;
     int rg = 2, ks = 0;
-    const int64_t units = int64_t(p.N / 32) * experts;
-    while (ks < most && (units << (ks + 1)) <= kSlots && (2 << ks) <= steps) ++ks;
-    if (!p.swiglu && (units << (ks + 1)) <= kSlots) rg = 1;
-    if (units > kSlots && steps >= 8) ks = 1;
+    while (ks < most && (units << (ks + 1)) <= slots && (2 << ks) <= steps) ++ks;
+    if (!p.swiglu && (units << (ks + 1)) <= slots) rg = 1;
+    if (units > slots && steps >= 8) ks = 1;
     p.ks_log2 = ks;
     return dtype == MOE_BF16 ? launch_x<__nv_bfloat16>(p, W->group, rg, nb, experts, stream)
                              : launch_x<__half>(p, W->group, rg, nb, experts, stream);
