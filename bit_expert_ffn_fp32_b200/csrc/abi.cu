@@ -14,4 +14,4 @@ MOE_API const char *moe_status_str(moe_status s) {
     return "MOE_ERR_UNKNOWN";
 }
 
-MOE_API int moe_version(void) { return 100; }
+MOE_API int moe_version(void) { return 200; }

@@ -359,7 +359,7 @@ def debug_wait_probe(counter, target: int, elapsed_ns, dev_status, stream=None) 
 class _Types:
     """torch's types and their moe_dtype codes, once torch is loaded."""
     code: dict = {}
-    int32 = device = None
+    int32 = device = raw_stream = None
 
     @classmethod
     def load(cls) -> None:
@@ -368,6 +368,7 @@ class _Types:
         cls.code = {torch.bfloat16: BF16, torch.int16: BF16, torch.float16: FP16, torch.float32: FP32}
         cls.int32 = torch.int32
         cls.device = torch.cuda.current_device
+        cls.raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def dtype_code(t) -> int:
@@ -396,6 +397,11 @@ def _table(t, n: int, dev: int) -> int | None:
     if t.dtype != _Types.int32:
         raise ValueError(f"an int32 tensor is wanted, got {t.dtype}")
     return _address(t, n, dev)
+
+
+def _stream_on(stream, dev: int) -> int | None:
+    """stream_handle where the current GPU is known."""
+    return (_Types.raw_stream(dev) if stream is None else stream.cuda_stream) or None
 
 
 def _place_of(t) -> int:
@@ -437,7 +443,7 @@ def linear_q4(W: Q4Weights, slot: int, x, T: int, out, act: int = ACT_NONE, stre
     dev = _place_of(W.tensors[0])
     code = lib.moe_linear_q4(C.addressof(W), slot, _address(x, T * W.K, dev), dtype_code(x), T, act,
                              _address(out, T * W.N // (1 + (act == ACT_SWIGLU)), dev), dtype_code(out),
-                             stream_handle(stream))
+                             _stream_on(stream, dev))
     if code:
         raise MoeError("moe_linear_q4", code)
 
@@ -452,7 +458,7 @@ def expert_linear_q4(W: Q4Weights, slot_of, x, T: int, E: int, k: int, offsets, 
                                     _table(offsets, E + 1, dev), _table(sorted_tok, P, dev),
                                     _table(active, E + 1, dev), act,
                                     _address(out, P * W.N // (1 + (act == ACT_SWIGLU)), dev), dtype_code(out),
-                                    _table(dev_status, 1, dev), stream_handle(stream))
+                                    _table(dev_status, 1, dev), _stream_on(stream, dev))
     if code:
         raise MoeError("moe_expert_linear_q4", code)
 
@@ -467,7 +473,7 @@ def expert_gemm(a, W, T: int, E: int, k: int, N: int, K: int, offsets, sorted_to
     code = lib.moe_expert_gemm(_address(a, (P if sorted_tok is None else T) * K, dev), _address(W, E * N * K, dev), dt,
                                T, E, k, N, K, _table(offsets, E + 1, dev), _table(sorted_tok, P, dev),
                                _address(out, P * N, dev), dtype_code(out), _table(dev_status, 1, dev),
-                               stream_handle(stream))
+                               _stream_on(stream, dev))
     if code:
         raise MoeError("moe_expert_gemm", code)
 
@@ -480,7 +486,7 @@ def expert_gemm_dgrad(dy, W, T: int, E: int, k: int, N: int, K: int, offsets, da
         raise ValueError("dy and W have one type")
     code = lib.moe_expert_gemm_dgrad(_address(dy, P * N, dev), _address(W, E * N * K, dev), dt, T, E, k, N, K,
                                      _table(offsets, E + 1, dev), _address(da, P * K, dev), dtype_code(da),
-                                     _table(dev_status, 1, dev), stream_handle(stream))
+                                     _table(dev_status, 1, dev), _stream_on(stream, dev))
     if code:
         raise MoeError("moe_expert_gemm_dgrad", code)
 
@@ -496,7 +502,7 @@ def expert_gemm_wgrad(dy, a, T: int, E: int, k: int, N: int, K: int, offsets, so
                                      dt, T, E, k, N, K, _table(offsets, E + 1, dev), _table(sorted_tok, P, dev),
                                      None if base is None else _address(base, E * N * K, dev),
                                      _address(dW, E * N * K, dev), odt, _table(dev_status, 1, dev),
-                                     stream_handle(stream))
+                                     _stream_on(stream, dev))
     if code:
         raise MoeError("moe_expert_gemm_wgrad", code)
 
@@ -507,7 +513,7 @@ def swiglu(gu, rows: int, f: int, h, stream=None) -> None:
     if dtype_code(h) != dt:
         raise ValueError("gu and h have one type")
     code = lib.moe_swiglu(_address(gu, rows * 2 * f, dev), dt, rows, f, _address(h, rows * f, dev),
-                          stream_handle(stream))
+                          _stream_on(stream, dev))
     if code:
         raise MoeError("moe_swiglu", code)
 
@@ -518,6 +524,6 @@ def swiglu_backward(gu, dh, rows: int, f: int, dgu, stream=None) -> None:
     if dtype_code(dh) != dt or dtype_code(dgu) != dt:
         raise ValueError("gu, dh and dgu have one type")
     code = lib.moe_swiglu_backward(_address(gu, rows * 2 * f, dev), _address(dh, rows * f, dev), dt, rows, f,
-                                   _address(dgu, rows * 2 * f, dev), stream_handle(stream))
+                                   _address(dgu, rows * 2 * f, dev), _stream_on(stream, dev))
     if code:
         raise MoeError("moe_swiglu_backward", code)

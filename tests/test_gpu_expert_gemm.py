@@ -315,6 +315,87 @@ def test_streams_graphs_and_repeats():
     assert_close(out, *forward_ref(a, W, offsets, tok))
 
 
+def test_two_calls_at_once():
+    """Two streams with their own tensors, many calls in flight on both."""
+    T, k, E, N, K = 300, 4, 12, 256, 320
+    sets = []
+    for seed in (1, 2):
+        _, offsets, tok, _ = route(T, k, E, seed=seed, crowd=0.3)
+        a, W, dy = rand((T, K), BF, seed), rand((E, N, K), BF, seed + 10), rand((T * k, N), BF, seed + 20)
+        outs = [(torch.empty(T * k, N, dtype=BF, device="cuda"), torch.empty(T * k, K, dtype=BF, device="cuda"),
+                 torch.empty(E, N, K, dtype=F32, device="cuda")) for _ in range(6)]
+        sets.append((offsets, tok, a, W, dy, outs, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(6):
+        for offsets, tok, a, W, dy, outs, stream in sets:
+            native.expert_gemm(a, W, T, E, k, N, K, offsets, tok, outs[i][0], stream=stream)
+            native.expert_gemm_dgrad(dy, W, T, E, k, N, K, offsets, outs[i][1], stream=stream)
+            native.expert_gemm_wgrad(dy, a, T, E, k, N, K, offsets, tok, outs[i][2], stream=stream)
+    torch.cuda.synchronize()
+    for offsets, tok, a, W, dy, outs, _ in sets:
+        assert_close(outs[0][0], *forward_ref(a, W, offsets, tok))
+        assert_close(outs[0][1], *dgrad_ref(dy, W, offsets))
+        assert_close(outs[0][2], *wgrad_ref(dy, a, E, offsets, tok))
+        for o in outs[1:]:
+            assert all(torch.equal(x, y) for x, y in zip(o, outs[0]))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sum_in_place_through_a_graph(dtype):
+    """Three replays add three times; integers, so that no sum is rounded."""
+    T, k, E, N, K = 40, 2, 8, 72, 136
+    _, offsets, tok, _ = route(T, k, E, seed=4, crowd=0.3)
+    g = torch.Generator().manual_seed(1)
+    dy = torch.randint(-1, 2, (T * k, N), generator=g).to(BF).cuda()
+    a = torch.randint(-1, 2, (T, K), generator=g).to(BF).cuda()
+    dW = torch.zeros(E, N, K, dtype=dtype, device="cuda")
+    native.expert_gemm_wgrad(dy, a, T, E, k, N, K, offsets, tok, dW)
+    once = dW.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        native.expert_gemm_wgrad(dy, a, T, E, k, N, K, offsets, tok, dW, base=dW)
+    for _ in range(2):
+        graph.replay()
+    assert torch.equal(dW, 3 * once) and torch.equal(once.double(), wgrad_ref(dy, a, E, offsets, tok)[0])
+
+
+@pytest.mark.parametrize("dtype,separate", [(BF, True), (BF, False), (F32, True), (F32, False)])
+def test_non_finite_sum_stays_in_its_place(dtype, separate):
+    T, k, E, N, K = 50, 2, 5, 72, 136
+    _, offsets, tok, _ = route(T, k, E, seed=4)
+    dy, a = rand((T * k, N), BF, 1), rand((T, K), BF, 2)
+    base = rand((E, N, K), dtype, 3)
+    dW = torch.empty_like(base)
+    native.expert_gemm_wgrad(dy, a, T, E, k, N, K, offsets, tok, dW, base=base)
+    spots = [(0, 0, 0), (1, 5, 77), (4, N - 1, K - 1)]
+    for i, s in enumerate(spots):
+        base[s] = float("nan") if i % 2 else float("inf")
+    out = torch.empty_like(base) if separate else base
+    native.expert_gemm_wgrad(dy, a, T, E, k, N, K, offsets, tok, out, base=base)
+    ok = torch.ones(E, N, K, dtype=torch.bool, device="cuda")
+    for s in spots:
+        ok[s] = False
+        assert not torch.isfinite(out[s])
+    assert torch.equal(out[ok], dW[ok])
+
+
+def test_bf16_bits_and_overflow():
+    """int16 tensors are bf16 bits; results past fp16 become infinities of their sign."""
+    T, k, E, N, K = 9, 2, 4, 64, 64
+    _, offsets, tok, _ = route(T, k, E, seed=4)
+    a, W = rand((T, K), BF, 1), rand((E, N, K), BF, 2)
+    out, bits = torch.empty(T * k, N, dtype=BF, device="cuda"), torch.empty(T * k, N, dtype=torch.int16, device="cuda")
+    forward(a, W, T, k, offsets, tok, out)
+    native.expert_gemm(a.view(torch.int16), W.view(torch.int16), T, E, k, N, K, offsets, tok, bits)
+    assert torch.equal(bits.view(BF), out)
+    big = torch.full((T, K), 200.0, dtype=FP, device="cuda")
+    Wb = torch.full((E, N, K), 100.0, dtype=FP, device="cuda")
+    Wb[:, 1::2] = -100.0
+    o = torch.empty(T * k, N, dtype=FP, device="cuda")
+    forward(big, Wb, T, k, offsets, tok, o)
+    assert (o[:, ::2] == float("inf")).all() and (o[:, 1::2] == -float("inf")).all()
+
+
 # ------------------------------------------------------------------ SwiGLU
 def swiglu_ref(gu, dh=None):
     f = gu.shape[1] // 2

@@ -222,6 +222,69 @@ def test_streams_graphs_and_repeats():
         assert torch.equal(out, want[0]) and torch.equal(many, want[1])
 
 
+def test_two_calls_at_once_and_bits():
+    """Two streams with their own tensors; int16 tensors are bf16 bits."""
+    T, N, K, group = 20, 512, 1024, 64
+    sets = []
+    for seed in (1, 2):
+        parts = make(2, N, K, group, True, seed)
+        sets.append((parts, native.q4_weights(*parts, group), rand((T, K), BF, seed),
+                     [torch.empty(T, N // 2, dtype=BF, device="cuda") for _ in range(8)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(8):
+        for _, W, x, outs, stream in sets:
+            if i % 2:
+                native.linear_q4(W, 1, x.view(torch.int16), T, outs[i].view(torch.int16), native.ACT_SWIGLU, stream)
+            else:
+                native.linear_q4(W, 1, x, T, outs[i], native.ACT_SWIGLU, stream)
+    torch.cuda.synchronize()
+    for parts, _, x, outs, _ in sets:
+        assert_close(outs[0], *reference(parts, group, native.ACT_SWIGLU, 1, x))
+        assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_many_experts_and_rows():
+    """As many experts as there may be, k = 16; and a batch of many passes."""
+    T, k, E, N, K, group = 90, 16, 4096, 32, 64, 32
+    _, offsets, tok, active = route(T, k, E, seed=3, crowd=0.4)
+    parts = make(E, N, K, group, False, 5)
+    slot_of = torch.arange(E - 1, -1, -1, dtype=torch.int32, device="cuda")
+    x = rand((T, K), BF, 1)
+    out = torch.empty(T * k, N, dtype=F32, device="cuda")
+    native.expert_linear_q4(native.q4_weights(*parts, group), slot_of, x, T, E, k, offsets, tok, active, out)
+    for e, r0, r1 in ranges(offsets)[::37] + ranges(offsets)[:1]:
+        assert_close(out[r0:r1], *reference(parts, group, 0, E - 1 - e, x[tok[r0:r1].long()]))
+    T = 1003
+    parts = make(1, 96, 288, 32, True, 6)
+    x, out = rand((T, 288), FP, 2), torch.empty(T, 96, dtype=FP, device="cuda")
+    native.linear_q4(native.q4_weights(*parts, 32), 0, x, T, out)
+    assert_close(out, *reference(parts, 32, 0, 0, x))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_outlier_in_a_row(dtype):
+    """One value 2^20 times the others, its weights 0: the others keep their digits
+    down to its share of the sums it passes through. Weights are formed as q and
+    -8, so it adds 8 s x and takes 8 s x off again. Each product instruction of
+    its group (4 of 16 k) aligns its 16 products and the sum so far to the largest
+    of them and cuts below 2^-23 of it: 17 cuts each; scaling, the group's sum of
+    x and the additions that join them round at most 8 times more. In all 76 times
+    2^-23 of 8 s 2^12, 0.3 s, where the others' results are about 0.4 s; losing
+    them to the outlier's own fp16 or bf16 step (2^12 * 2^-8 and more) is 16 s."""
+    N, K, group = 64, 512, 64
+    codes, scale, _ = make(1, N, K, group, False, 8)
+    codes[0, :, 50] = 0x88                               # weights 100 and 101 are 0
+    x = rand((3, K), dtype, 1, 2.0 ** -8)
+    x[:, 100] = 2.0 ** 12
+    out = torch.empty(3, N, dtype=F32, device="cuda")
+    native.linear_q4(native.q4_weights(codes, scale, None, group), 0, x, 3, out)
+    x0 = x.clone()
+    x0[:, 100] = 0
+    y, tol = reference((codes, scale, None), group, 0, 0, x0)
+    s = scale[0, :, 1].double()
+    assert_close(out, y, tol + 76 * 2.0 ** -23 * 8 * 2.0 ** 12 * s)
+
+
 def test_codes_past_32_bit_offsets():
     slots, N, K, group = 66, 8192, 8192, 128            # 2.2e9 bytes of codes
     codes = torch.randint(0, 256, (slots, N, K // 2), dtype=torch.uint8, device="cuda")
