@@ -28,6 +28,31 @@ inline moe_status launch_status() {
     return MOE_OK;
 }
 
+// A launch that may be set up while the work before it on the stream still runs
+// (kernels that begin with after_previous()); shared by the calls that follow
+// one another in decoding, where a launch is a good part of the time.
+inline cudaError_t launch_early(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attrs)[2], int clusters, const void *fn,
+                                void **args) {
+    int n = 0;
+    attrs[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[n++].val.programmaticStreamSerializationAllowed = 1;
+    if (clusters > 1) {
+        attrs[n].id = cudaLaunchAttributeClusterDimension;
+        attrs[n].val.clusterDim.x = clusters;
+        attrs[n].val.clusterDim.y = attrs[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attrs;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+// First thing in such a kernel, by every thread: from here on everything before
+// it on the stream is done and visible; what follows it may be set up as well.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ void flag(int32_t *status, int bit) {
     if (status) atomicOr(status, bit);
 }

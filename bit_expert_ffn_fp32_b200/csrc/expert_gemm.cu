@@ -790,6 +790,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (C::CG == 2) tc::tmem_alloc_pair(&s.tmem_base, C::kCols);
         else tc::tmem_alloc(&s.tmem_base, C::kCols);
     }
+    after_previous();
     Entry *table = reinterpret_cast<Entry *>(dyn + p.stages * C::kStage + kEpiWarps * kTurn * (1 + p.read_base));
     const int total = build_table<C>(p, s, table, MT);
     tc::fence_before();
@@ -906,13 +907,9 @@ moe_status launch(GemmParams &p, const GemmMaps &maps, int64_t most_tiles, int s
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = C::CG;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = C::CG > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, expert_gemm_kernel<C>, p, maps) != cudaSuccess) {
+    cudaLaunchAttribute attrs[2];
+    void *args[] = {&p, const_cast<GemmMaps *>(&maps)};
+    if (launch_early(cfg, attrs, C::CG, reinterpret_cast<const void *>(expert_gemm_kernel<C>), args) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }

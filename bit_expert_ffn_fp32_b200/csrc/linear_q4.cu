@@ -117,6 +117,7 @@ __device__ __forceinline__ float half_at(const uint4 &v, int j) {
 // rows); NB: tiles of 8 tokens whose sums a warp keeps.
 template <typename X, int G, int RG, int NB>
 __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const __grid_constant__ Q4Params p) {
+    after_previous();
     constexpr int R = 16 * RG, W = G / 32, J = kStep / G;
     extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -488,8 +489,18 @@ moe_status launch(Q4Params &p, int experts, cudaStream_t stream) {
         return MOE_ERR_CUDA;
     }
     const int units = p.swiglu ? p.N / 32 : p.N / (16 * RG), per_block = kWarps >> p.ks_log2;
-    q4_kernel<X, G, RG, NB><<<dim3((units + per_block - 1) / per_block, experts), 32 * kWarps, smem, stream>>>(p);
-    return launch_status();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((units + per_block - 1) / per_block, experts);
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    void *args[] = {&p};
+    if (launch_early(cfg, attrs, 1, reinterpret_cast<const void *>(q4_kernel<X, G, RG, NB>), args) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
 }
 
 template <typename X, int G>

@@ -58,6 +58,7 @@ __device__ __forceinline__ Where where(int64_t row0, uint32_t chunk0, uint32_t i
 template <typename E, bool BACKWARD>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const E *gu, const E *__restrict__ dh, int64_t chunks, int f,
                                                           uint32_t div, E *out) {
+    after_previous();
     const uint32_t cr = uint32_t(f) / 8;
     const int64_t first = int64_t(blockIdx.x) * kTile, row0 = first / cr;
     const uint32_t chunk0 = uint32_t(first - row0 * cr);
@@ -107,10 +108,19 @@ moe_status launch(const void *gu, const void *dh, int64_t rows, int f, void *out
     const int64_t chunks = rows * (f / 8), blocks = (chunks + kTile - 1) / kTile;
     if (blocks >= (int64_t(1) << 31)) return MOE_ERR_OVERFLOW;
     const uint64_t cr = uint64_t(f) / 8;
-    swiglu_kernel<E, BACKWARD><<<unsigned(blocks), kThreads, 0, stream>>>(
-        static_cast<const E *>(gu), static_cast<const E *>(dh), chunks, f,
-        uint32_t(((uint64_t(1) << 32) + cr - 1) / cr), static_cast<E *>(out));
-    return launch_status();
+    uint32_t div = uint32_t(((uint64_t(1) << 32) + cr - 1) / cr);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(blocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    int64_t n = chunks;
+    void *args[] = {&gu, &dh, &n, &f, &div, &out};
+    if (launch_early(cfg, attrs, 1, reinterpret_cast<const void *>(swiglu_kernel<E, BACKWARD>), args) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
 }
 
 moe_status check_swiglu(int dtype, int64_t rows, int f) {
