@@ -33,7 +33,8 @@
  *  - Calls keep no state between invocations and may run concurrently on
  *    different streams with disjoint outputs.
  *  - Shapes: d and f multiples of 256 (d <= 8192, f <= 8192), 1 <= k <= 16,
- *    k <= E <= 4096, T*k < 2^31.
+ *    k <= E <= 4096, T*k < 2^31. The 4-bit and the unquantised products state
+ *    their own N and K.
  */
 #ifndef MOE_H
 #define MOE_H
