@@ -7,8 +7,9 @@
 // chunks of 8 elements (16-byte loads of every operand, all issued before the
 // first is used), a block 512 chunks in a row; blocks are not persistent, so
 // the loads of one cover the stores of another. sig(g) is formed with the
-// hardware's exp2 and reciprocal (a few units of 2^-22, against half a step of
-// 2^-11 or 2^-8 in the result).
+// hardware's exp2 and reciprocal: off by about 2^-22 + |g| 2^-24, at most 2^-16
+// where exp still answers, against half a step of 2^-11 (fp16, whose products
+// vanish long before) or 2^-8 in the result.
 #include <algorithm>
 
 #include "common.cuh"
@@ -37,8 +38,12 @@ struct Pack2<__half> {
     }
 };
 
-// 1 / (1 + exp(-g)); 0 where exp(-g) passes 2^126, 1 for large g.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + exp(-g)), for g < 0 as exp(g) / (1 + exp(g)): no overflow on the way,
+// so a far gate keeps its share of a large u down to exp's smallest subnormal.
+__device__ __forceinline__ float sigmoid(float g) {
+    const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e);
+    return g < 0.f ? e * r : r;
+}
 
 // Chunk i of this block's tile: its row, and its first element in the row.
 // chunks_of_row = f / 8; div = ceil(2^32 / chunks_of_row) divides the small

@@ -449,3 +449,20 @@ def test_swiglu_far_values():
     # products below fp32's normal range may be flushed: 88 * 2^-126 at most
     assert_close(h, want, want.abs() * 2.0 ** -18 + 2.0 ** -119)
     assert_close(dgu, dwant, dwant.abs() * 2.0 ** -18 + 2.0 ** -119)
+
+
+def test_swiglu_far_gate_of_a_large_product():
+    """exp(-g) beyond fp32's largest power of two: the product with a large u is
+    not far from one, so sig(g) may not vanish on the way."""
+    # exp(g), g = -90..-87.5: its argument in powers of two (130) is off by 2^-17 + 2^-18, exp by 0.7 of that; the
+    # subnormal exp of 2^-130 keeps 19 bits; together below 2^-15.9, a few roundings of 2^-24 on top
+    g = torch.tensor([[-87.5, -88.0, -88.5, -88.75, -89.0, -89.25, -89.5, -90.0]], device="cuda").to(BF)
+    u = torch.full_like(g, 2.0 ** 124)
+    gu, dh = torch.cat((g, u), dim=1), torch.full_like(g, 2.0 ** 1)
+    h, dgu = torch.empty(1, 8, dtype=BF, device="cuda"), torch.empty(1, 16, dtype=BF, device="cuda")
+    native.swiglu(gu, 1, 8, h)
+    native.swiglu_backward(gu, dh, 1, 8, dgu)
+    want, dwant = swiglu_ref(gu), swiglu_ref(gu, dh)
+    assert (want.abs() > 0.1).all()
+    assert_close(h, want, want.abs() * 2.0 ** -15)
+    assert_close(dgu, dwant, dwant.abs() * 2.0 ** -15)
