@@ -15,6 +15,8 @@ namespace moe {
 constexpr int kMaxE = 4096;
 constexpr int kMaxK = 16;
 constexpr int kMaxDim = 8192;
+// Pairs of the 4-bit and the unquantised products: row numbers rounded up to a tile stay in 32 bits.
+constexpr int64_t kMaxPairs = (int64_t(1) << 31) - 4096;
 
 inline cudaStream_t as_cuda(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 

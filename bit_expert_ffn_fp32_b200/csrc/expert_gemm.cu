@@ -19,9 +19,16 @@
 // zeros there, as they are summed): those are written by gathering warps with
 // 16-byte cp.async in the same swizzle (gathering TMA loads of four rows took
 // about 48 cycles each, ten bytes a cycle). Warps: TMA, MMA issue, eight for
-// the epilogue, eight that gather and one that hands their stages on; two
-// accumulators, so that the epilogue of one tile runs beside the products of
-// the next. Every wait is bounded and sets MOE_DEV_TIMEOUT.
+// the epilogue, eight (wgrad: four) that gather and one that hands their stages
+// on; two accumulators, so that the epilogue of one tile runs beside the
+// products of the next. Every wait is bounded and sets MOE_DEV_TIMEOUT.
+//
+// Measured (device time of a call): 81,920 pairs by token, 512 experts, 1536 x
+// 2048: 690 us, 78% of the copy bandwidth on its 3.5 GB; dgrad of 4096 tokens,
+// top-10 of 128 experts, the same weights: 216 us at 1.5 GHz (tensor pipe 67%
+// active, DRAM 61%); wgrad of 2048 x 768 for them: 150 us, where MMA and
+// epilogue take turns (5.6 stages a tile); four tokens through 2048 x 768 in
+// fp32: 26 us, 73% of the copy bandwidth.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -42,7 +49,7 @@ constexpr int kTileI = 64;       // contracted index a stage: 128 bytes, one swi
 constexpr int kLoadWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 8, kPickWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kPickThreads = 128;  // gathering threads that fill a stage
 constexpr int kMaxStages = 10;
-constexpr int kTurn = 2048;      // per epilogue warp: 32 x 32 16-bit values on their way to 16-byte stores
+constexpr int kTurn = 2048;      // per epilogue warp: a box of results on its way out
 constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
 
 struct GemmParams {
@@ -94,8 +101,7 @@ struct Cfg {
     static constexpr int kThreads = 32 * (PICK ? kRelayWarp + 1 : kPickWarp0);
     static constexpr int kBRows = TN / CG;  // of B a CTA holds
     static constexpr int kA = kTileM * 128, kB = kBRows * 128, kStage = kA + kB;
-    // shared memory: the ring, the epilogue's turning space, the table of E + 1 entries
-    // (twice with a sum to read)
+    // shared memory: the ring, the epilogue's boxes (twice with a sum to read), the table of E + 1 entries
     static constexpr size_t fixed(int E, int read_base) {
         return kEpiWarps * kTurn * (1 + read_base) + (size_t(E) + 1) * sizeof(Entry) + 1024;
     }
@@ -109,7 +115,8 @@ struct Cfg {
     // instead of round, an error that grows with the length of a chain. Narrow
     // tiles have room for four in each buffer; wide ones take both buffers.
     static constexpr int kAccs = CG == 1 ? 4 : 2, kBuf = CG == 1 ? kAccs * TN : TN, kCols = 2 * kBuf;
-    static_assert(stages(kMaxE, PASS == kWgrad) >= 4 && sizeof(GemmSmem) <= 1024 && kCols >= 32 && kCols <= 512, "tile does not fit");
+    static_assert(stages(kMaxE, PASS == kWgrad) >= 4 && sizeof(GemmSmem) <= 1024 && kCols >= 32 && kCols <= 512,
+                  "tile does not fit");
 };
 
 __device__ __forceinline__ void stop(GemmSmem &s, int32_t *status) {
@@ -199,7 +206,7 @@ struct Walk {
         Tile t;
         t.e = x.e, t.r0 = x.r0, t.rows = x.rows;
         const int local = tau - x.tile;
-        int j = int(float(local) * inv_mt);  // local / MT, off by one at most
+        int j = local / (1 << 22) ? local / MT : int(float(local) * inv_mt);  // local / MT, off by one at most
         j += (j + 1) * MT <= local;
         j -= j * MT > local;
         t.m0 = ((local - j * MT) * C::CG + rank) * kTileM;
@@ -255,7 +262,8 @@ struct Ring {
 // TMA warp: fills stage after stage, all tiles of this CTA in a row. The bytes
 // of both CTAs of a pair count on rank 0's barrier.
 template <typename C>
-__device__ void load_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &m, unsigned char *dyn, Walk<C> walk, int total) {
+__device__ void load_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &m, unsigned char *dyn, Walk<C> walk,
+                           int total) {
     Ring at(p.stages);
     int it = 0;
     bool ok = true;
@@ -736,7 +744,8 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &ma
         if (ADD && any) to.want(t, m1, 32 * half);
         bool ok = true;
         if (accs) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.tfull[buf], phase, kWaitNs));
+            // a tile of many stages may rightly take longer than one wait
+            ok = tc::mbar_wait_warp(&s.tfull[buf], phase, kWaitNs + 2000ull * KS);
             tc::fence_after();
             ++count;
         }
@@ -977,7 +986,7 @@ moe_status check_gemm(int dtype, int T, int E, int k, int N, int K, int out_dtyp
     if (!half_type(dtype) || !out_type_ok(dtype, out_dtype)) return MOE_ERR_INVALID_ARG;
     if (E > kMaxE || k > kMaxK || k > E) return MOE_ERR_UNSUPPORTED;
     if (N % 8 || K % 8 || N > 2 * kMaxDim || K > 2 * kMaxDim) return MOE_ERR_UNSUPPORTED;
-    if (int64_t(T) * k >= (int64_t(1) << 31)) return MOE_ERR_OVERFLOW;
+    if (int64_t(T) * k > kMaxPairs) return MOE_ERR_OVERFLOW;
     return MOE_OK;
 }
 

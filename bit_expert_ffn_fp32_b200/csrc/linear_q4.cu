@@ -224,220 +224,220 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[nb][rg][i] = 0.f;
         for (int c0 = 0; c0 < steps; c0 += p.chunk) {
-        // stage x: a code word's halves hold codes j and j + 4, so k j and k j + 4 share a register of x; those of
-        // odd j scaled down by the 2^4 that their codes are high
-        const int quads = min(p.chunk * (kStep / 32), p.K / 32 - c0 * (kStep / 32)), cgroups = quads * 32 / G;  // of 32 k
-        const int quads4 = (quads + 3) & ~3;  // of whole 128 k, so that the four of one stay together
-        if (c0) __syncthreads();
-        // one token's 32 k: lanes of one token are TS apart, so the sums and the largest of 128 k are a shuffle away
-        const int all = (tiles * quads4 << ts) + 31 & ~31;
-        auto load = [&](int i, uint4(&v)[4]) {
-            const int tq = i >> ts, nb = tq / quads4, quad = tq - nb * quads4, tok = 8 * nb + (i & (TS - 1));
-            int row = -1;
-            if (nb < tiles && quad < quads && tok < n) {
-                row = pass + tok;
-                if (p.sorted_tok) {
-                    row = p.sorted_tok[row];
-                    if (row < 0 || row >= p.T) {
-                        if (blockIdx.x == 0 && quad == 0) flag(p.status, MOE_DEV_BAD_INDEX);
-                        row = -1;
+            // stage x: a code word's halves hold codes j and j + 4, so k j and k j + 4 share a register of x; those of
+            // odd j scaled down by the 2^4 that their codes are high
+            const int quads = min(p.chunk * (kStep / 32), p.K / 32 - c0 * (kStep / 32)), cgroups = quads * 32 / G;  // of 32 k
+            const int quads4 = (quads + 3) & ~3;  // of whole 128 k, so that the four of one stay together
+            if (c0) __syncthreads();
+            // one token's 32 k: lanes of one token are TS apart, so the sums and the largest of 128 k are a shuffle away
+            const int all = (tiles * quads4 << ts) + 31 & ~31;
+            auto load = [&](int i, uint4(&v)[4]) {
+                const int tq = i >> ts, nb = tq / quads4, quad = tq - nb * quads4, tok = 8 * nb + (i & (TS - 1));
+                int row = -1;
+                if (nb < tiles && quad < quads && tok < n) {
+                    row = pass + tok;
+                    if (p.sorted_tok) {
+                        row = p.sorted_tok[row];
+                        if (row < 0 || row >= p.T) {
+                            if (blockIdx.x == 0 && quad == 0) flag(p.status, MOE_DEV_BAD_INDEX);
+                            row = -1;
+                        }
                     }
                 }
-            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
-            if (row >= 0) {
-                const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const X *>(p.x) + int64_t(row) * p.K) +
-                                    (c0 * (kStep / 32) + quad) * 4;
+                for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
+                if (row >= 0) {
+                    const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const X *>(p.x) + int64_t(row) * p.K) +
+                                        (c0 * (kStep / 32) + quad) * 4;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = __ldg(from + k);
-            }
-        };
-        uint4 next[4];
-        if (int(threadIdx.x) < all) load(threadIdx.x, next);
-        for (int i = threadIdx.x; i < all; i += 32 * kWarps) {
-            const int tq = i >> ts, nb = tq / quads4, quad = tq - nb * quads4;
-            uint4 v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = next[k];
-            if (i + 32 * kWarps < all) load(i + 32 * kWarps, next);  // on its way while these are scaled
-            // the power of two of these 128 k: 14 less the exponent of their largest
-            float x[4][8], most = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const X *h = reinterpret_cast<const X *>(&v[k]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[k][j] = to_f32(h[j]);
-                    most = fmaxf(most, fabsf(x[k][j]));
+                    for (int k = 0; k < 4; ++k) v[k] = __ldg(from + k);
                 }
-            }
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, TS));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2 * TS));
-            const int e = min(14 - (int(__float_as_uint(most) >> 23) - 127), 100);
-            const float up = __uint_as_float(uint32_t(127 + e) << 23);
-            float part = 0.f;
+            };
+            uint4 next[4];
+            if (int(threadIdx.x) < all) load(threadIdx.x, next);
+            for (int i = threadIdx.x; i < all; i += 32 * kWarps) {
+                const int tq = i >> ts, nb = tq / quads4, quad = tq - nb * quads4;
+                uint4 v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float eight = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[k][j] *= up;
-                    eight += x[k][j];
-                }
-                part += eight;
-            }
-            if (G >= 64) part += __shfl_xor_sync(0xffffffffu, part, TS);
-            if (G >= 128) part += __shfl_xor_sync(0xffffffffu, part, 2 * TS);
-            if (nb < tiles && quad < quads) {
-                const int slot8 = i & (TS - 1);
-                if ((quad & (G / 32 - 1)) == 0) xsum[(nb * cgroups + quad / (G / 32)) * 8 + slot8] = part;
-                if ((quad & 3) == 0)
-                    xdown[(nb * p.chunk * 2 + quad / 4) * 8 + slot8] = __uint_as_float(uint32_t(127 - e) << 23);
+                for (int k = 0; k < 4; ++k) v[k] = next[k];
+                if (i + 32 * kWarps < all) load(i + 32 * kWarps, next);  // on its way while these are scaled
+                // the power of two of these 128 k: 14 less the exponent of their largest
+                float x[4][8], most = 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int unit8 = quad * 4 + k, q = unit8 & (G / 8 - 1);
-                    const int at = (unit8 & ~(G / 8 - 1)) + (q % W) * 4 + q / W;
-                    uint32_t h[4];
+                    const X *h = reinterpret_cast<const X *>(&v[k]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float f = j & 1 ? 0.0625f : 1.f;
-                        const __half2 two = __floats2half2_rn(x[k][j] * f, x[k][j + 4] * f);
-                        h[j] = *reinterpret_cast<const uint32_t *>(&two);
+                    for (int j = 0; j < 8; ++j) {
+                        x[k][j] = to_f32(h[j]);
+                        most = fmaxf(most, fabsf(x[k][j]));
                     }
-                    xs[nb * tile_units + (at << ts) + slot8] = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, TS));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2 * TS));
+                const int e = min(14 - (int(__float_as_uint(most) >> 23) - 127), 100);
+                const float up = __uint_as_float(uint32_t(127 + e) << 23);
+                float part = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float eight = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        x[k][j] *= up;
+                        eight += x[k][j];
+                    }
+                    part += eight;
+                }
+                if (G >= 64) part += __shfl_xor_sync(0xffffffffu, part, TS);
+                if (G >= 128) part += __shfl_xor_sync(0xffffffffu, part, 2 * TS);
+                if (nb < tiles && quad < quads) {
+                    const int slot8 = i & (TS - 1);
+                    if ((quad & (G / 32 - 1)) == 0) xsum[(nb * cgroups + quad / (G / 32)) * 8 + slot8] = part;
+                    if ((quad & 3) == 0)
+                        xdown[(nb * p.chunk * 2 + quad / 4) * 8 + slot8] = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int unit8 = quad * 4 + k, q = unit8 & (G / 8 - 1);
+                        const int at = (unit8 & ~(G / 8 - 1)) + (q % W) * 4 + q / W;
+                        uint32_t h[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float f = j & 1 ? 0.0625f : 1.f;
+                            const __half2 two = __floats2half2_rn(x[k][j] * f, x[k][j + 4] * f);
+                            h[j] = *reinterpret_cast<const uint32_t *>(&two);
+                        }
+                        xs[nb * tile_units + (at << ts) + slot8] = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
                 }
             }
-        }
-        __syncthreads();
-        for (int step0 = c0 + ks; step0 < min(steps, c0 + p.chunk); step0 += kDepth * KS) {
+            __syncthreads();
+            for (int step0 = c0 + ks; step0 < min(steps, c0 + p.chunk); step0 += kDepth * KS) {
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                const int step = step0 + d * KS;
-                if (step < steps && busy) {
-                    tc::cp_async_wait<kDepth - 1>();
-                    if (RG == 2 || lane < 16) {  // scale pairs of this lane's row
-                        float2 *own = reinterpret_cast<float2 *>(pairs) + (lane >> 4) * 16 + 2 * (lane & 7) +
-                                      ((lane >> 3) & 1);
+                for (int d = 0; d < kDepth; ++d) {
+                    const int step = step0 + d * KS;
+                    if (step < steps && busy) {
+                        tc::cp_async_wait<kDepth - 1>();
+                        if (RG == 2 || lane < 16) {  // scale pairs of this lane's row
+                            float2 *own = reinterpret_cast<float2 *>(pairs) + (lane >> 4) * 16 + 2 * (lane & 7) +
+                                          ((lane >> 3) & 1);
 #pragma unroll
-                        for (int j = 0; j < J; ++j) {
-                            const float s = half_at(sc[d], j);
-                            own[j * R] = make_float2(s * 16777216.f, p.min ? half_at(mn[d], j) : -8.f * s);
-                        }
-                    }
-                    __syncwarp();
-                    const unsigned char *st = mine + d * (R * 128) + g * 128;
-                    const uint4 *xstep = xs + (((step - c0) * (kStep / 8) + t) << ts) + (g & (TS - 1));
-                    // adds group j to y, in the scale of its 128 k
-                    auto group = [&](int j, float(&y)[NB][RG][4]) {
-                        uint32_t w[RG][2][W];
-#pragma unroll
-                        for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                // bytes (G / 8) t of the group's G / 2, in swizzled 16-byte chunks
-                                const int byte = j * (G / 2) + (G / 8) * t;
-                                const unsigned char *from = st + (16 * rg + 8 * i) * 128 +
-                                                            (((byte >> 4) ^ swizzle<G>(g)) << 4) + (byte & 15);
-                                if constexpr (W == 1) {
-                                    w[rg][i][0] = *reinterpret_cast<const uint32_t *>(from);
-                                } else if constexpr (W == 2) {
-                                    const uint2 v = *reinterpret_cast<const uint2 *>(from);
-                                    w[rg][i][0] = v.x, w[rg][i][1] = v.y;
-                                } else {
-                                    const uint4 v = *reinterpret_cast<const uint4 *>(from);
-                                    w[rg][i][0] = v.x, w[rg][i][1] = v.y, w[rg][i][2] = v.z, w[rg][i][3] = v.w;
-                                }
+                            for (int j = 0; j < J; ++j) {
+                                const float s = half_at(sc[d], j);
+                                own[j * R] = make_float2(s * 16777216.f, p.min ? half_at(mn[d], j) : -8.f * s);
                             }
-                        float acc[NB][RG][4];
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
+                        }
+                        __syncwarp();
+                        const unsigned char *st = mine + d * (R * 128) + g * 128;
+                        const uint4 *xstep = xs + (((step - c0) * (kStep / 8) + t) << ts) + (g & (TS - 1));
+                        // adds group j to y, in the scale of its 128 k
+                        auto group = [&](int j, float(&y)[NB][RG][4]) {
+                            uint32_t w[RG][2][W];
 #pragma unroll
                             for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) acc[nb][rg][i] = 0.f;
+                                for (int i = 0; i < 2; ++i) {
+                                    // bytes (G / 8) t of the group's G / 2, in swizzled 16-byte chunks
+                                    const int byte = j * (G / 2) + (G / 8) * t;
+                                    const unsigned char *from = st + (16 * rg + 8 * i) * 128 +
+                                                                (((byte >> 4) ^ swizzle<G>(g)) << 4) + (byte & 15);
+                                    if constexpr (W == 1) {
+                                        w[rg][i][0] = *reinterpret_cast<const uint32_t *>(from);
+                                    } else if constexpr (W == 2) {
+                                        const uint2 v = *reinterpret_cast<const uint2 *>(from);
+                                        w[rg][i][0] = v.x, w[rg][i][1] = v.y;
+                                    } else {
+                                        const uint4 v = *reinterpret_cast<const uint4 *>(from);
+                                        w[rg][i][0] = v.x, w[rg][i][1] = v.y, w[rg][i][2] = v.z, w[rg][i][3] = v.w;
+                                    }
+                                }
+                            float acc[NB][RG][4];
 #pragma unroll
-                        for (int wi = 0; wi < W; ++wi) {
-                            uint32_t lo[RG][4], hi[RG][4];
+                            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                            for (int rg = 0; rg < RG; ++rg) {
-                                halves_of(w[rg][0][wi], lo[rg]);
-                                halves_of(w[rg][1][wi], hi[rg]);
-                            }
+                                for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) {
-                                if (NB > 1 && nb >= tiles) break;
-                                const uint4 xv = xstep[nb * tile_units + ((j * W + wi) * 4 << ts)];
+                                    for (int i = 0; i < 4; ++i) acc[nb][rg][i] = 0.f;
+#pragma unroll
+                            for (int wi = 0; wi < W; ++wi) {
+                                uint32_t lo[RG][4], hi[RG][4];
 #pragma unroll
                                 for (int rg = 0; rg < RG; ++rg) {
-                                    mma_fp16(acc[nb][rg], lo[rg][0], hi[rg][0], lo[rg][1], hi[rg][1], xv.x, xv.y);
-                                    mma_fp16(acc[nb][rg], lo[rg][2], hi[rg][2], lo[rg][3], hi[rg][3], xv.z, xv.w);
+                                    halves_of(w[rg][0][wi], lo[rg]);
+                                    halves_of(w[rg][1][wi], hi[rg]);
+                                }
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb) {
+                                    if (NB > 1 && nb >= tiles) break;
+                                    const uint4 xv = xstep[nb * tile_units + ((j * W + wi) * 4 << ts)];
+#pragma unroll
+                                    for (int rg = 0; rg < RG; ++rg) {
+                                        mma_fp16(acc[nb][rg], lo[rg][0], hi[rg][0], lo[rg][1], hi[rg][1], xv.x, xv.y);
+                                        mma_fp16(acc[nb][rg], lo[rg][2], hi[rg][2], lo[rg][3], hi[rg][3], xv.z, xv.w);
+                                    }
                                 }
                             }
-                        }
-                        float2 x01[NB];
+                            float2 x01[NB];
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-                            if (NB == 1 || nb < tiles)
-                                x01[nb] = *reinterpret_cast<const float2 *>(
-                                    xsum + (nb * cgroups + (step - c0) * J + j) * 8 + 2 * t);
+                            for (int nb = 0; nb < NB; ++nb)
+                                if (NB == 1 || nb < tiles)
+                                    x01[nb] = *reinterpret_cast<const float2 *>(
+                                        xsum + (nb * cgroups + (step - c0) * J + j) * 8 + 2 * t);
 #pragma unroll
-                        for (int rg = 0; rg < RG; ++rg) {
-                            const float4 f = pairs[(j * RG + rg) * 8 + g];  // s 2^24, m of row g, then of row g + 8
+                            for (int rg = 0; rg < RG; ++rg) {
+                                const float4 f = pairs[(j * RG + rg) * 8 + g];  // s 2^24, m of row g, then of row g + 8
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb) {
+                                    if (NB > 1 && nb >= tiles) break;
+                                    float(&o)[4] = y[nb][rg];
+                                    const float(&v)[4] = acc[nb][rg];
+                                    o[0] = fmaf(f.x, v[0], fmaf(f.y, x01[nb].x, o[0]));
+                                    o[1] = fmaf(f.x, v[1], fmaf(f.y, x01[nb].y, o[1]));
+                                    o[2] = fmaf(f.z, v[2], fmaf(f.w, x01[nb].x, o[2]));
+                                    o[3] = fmaf(f.z, v[3], fmaf(f.w, x01[nb].y, o[3]));
+                                }
+                            }
+                        };
+                        // `count` groups of 128 k, then out of their scale
+                        auto half_step = [&](int h, int count, bool whole) {
+                            float y[NB][RG][4];
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) y[nb][rg][i] = 0.f;
+                            if (whole) {
+#pragma unroll
+                                for (int j = 0; j < J / 2; ++j) group(h * (J / 2) + j, y);
+                            } else {
+#pragma unroll 1
+                                for (int j = 0; j < count; ++j) group(h * (J / 2) + j, y);
+                            }
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb) {
                                 if (NB > 1 && nb >= tiles) break;
-                                float(&o)[4] = y[nb][rg];
-                                const float(&v)[4] = acc[nb][rg];
-                                o[0] = fmaf(f.x, v[0], fmaf(f.y, x01[nb].x, o[0]));
-                                o[1] = fmaf(f.x, v[1], fmaf(f.y, x01[nb].y, o[1]));
-                                o[2] = fmaf(f.z, v[2], fmaf(f.w, x01[nb].x, o[2]));
-                                o[3] = fmaf(f.z, v[3], fmaf(f.w, x01[nb].y, o[3]));
+                                const float2 down = *reinterpret_cast<const float2 *>(
+                                    xdown + ((nb * p.chunk + step - c0) * 2 + h) * 8 + 2 * t);
+#pragma unroll
+                                for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        sum[nb][rg][i] = fmaf(i & 1 ? down.y : down.x, y[nb][rg][i], sum[nb][rg][i]);
                             }
-                        }
-                    };
-                    // `count` groups of 128 k, then out of their scale
-                    auto half_step = [&](int h, int count, bool whole) {
-                        float y[NB][RG][4];
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                            for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) y[nb][rg][i] = 0.f;
-                        if (whole) {
-#pragma unroll
-                            for (int j = 0; j < J / 2; ++j) group(h * (J / 2) + j, y);
+                        };
+                        const int here = groups - step * J;
+                        if (here >= J) {  // in one piece, so that the groups' products overlap
+                            half_step(0, J / 2, true);
+                            half_step(1, J / 2, true);
                         } else {
-#pragma unroll 1
-                            for (int j = 0; j < count; ++j) group(h * (J / 2) + j, y);
+                            half_step(0, min(here, J / 2), false);
+                            if (here > J / 2) half_step(1, here - J / 2, false);
                         }
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            if (NB > 1 && nb >= tiles) break;
-                            const float2 down = *reinterpret_cast<const float2 *>(
-                                xdown + ((nb * p.chunk + step - c0) * 2 + h) * 8 + 2 * t);
-#pragma unroll
-                            for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    sum[nb][rg][i] = fmaf(i & 1 ? down.y : down.x, y[nb][rg][i], sum[nb][rg][i]);
-                        }
-                    };
-                    const int here = groups - step * J;
-                    if (here >= J) {  // in one piece, so that the groups' products overlap
-                        half_step(0, J / 2, true);
-                        half_step(1, J / 2, true);
-                    } else {
-                        half_step(0, min(here, J / 2), false);
-                        if (here > J / 2) half_step(1, here - J / 2, false);
+                        __syncwarp();  // every lane has read the stage before it is refilled
+                        issue(step + kDepth * KS, d);
+                        issue_scales(step + kDepth * KS, sc[d], mn[d]);
                     }
-                    __syncwarp();  // every lane has read the stage before it is refilled
-                    issue(step + kDepth * KS, d);
-                    issue_scales(step + kDepth * KS, sc[d], mn[d]);
                 }
             }
-        }
         }
         tc::cp_async_wait<0>();
         __syncthreads();  // the rings are free: partial sums [token][row] take their place
@@ -481,7 +481,8 @@ moe_status launch(Q4Params &p, int experts, cudaStream_t stream) {
     const int steps = (p.K + kStep - 1) / kStep, unit = kDepth << p.ks_log2, per_step = NB * (kStep * 2 << p.ts_log2);
     const int whole = (steps + unit - 1) / unit, fit = (NB == 1 ? 36 : 128) * 1024 / (per_step * unit);
     p.chunk = std::max(1, std::min(whole, fit)) * unit;
-    const size_t smem = size_t(kWarps) * kWarpBytes<G, RG, NB> + size_t(p.chunk) * (per_step + NB * (kStep / G) * 32 + NB * 64);
+    const size_t smem = size_t(kWarps) * kWarpBytes<G, RG, NB> +
+                        size_t(p.chunk) * (per_step + NB * (kStep / G) * 32 + NB * 64);
     // set on every call: the attribute belongs to the current device's context
     if (smem > 232448 || cudaFuncSetAttribute(q4_kernel<X, G, RG, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               int(smem)) != cudaSuccess) {
@@ -583,6 +584,7 @@ MOE_API moe_status moe_linear_q4(const moe_q4weights *W, int32_t slot, const voi
     const moe_status st = check_q4(W, dtype, act, out_dtype);
     if (st != MOE_OK) return st;
     if (T < 0 || slot < 0 || slot >= W->num_slots) return MOE_ERR_INVALID_ARG;
+    if (T > kMaxPairs) return MOE_ERR_OVERFLOW;
     if (T == 0) return MOE_OK;
     if (!x || !out || !aligned16(x) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
     Q4Params p = {};
@@ -600,7 +602,7 @@ MOE_API moe_status moe_expert_linear_q4(const moe_q4weights *W, const int32_t *s
     if (st != MOE_OK) return st;
     if (T < 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
     if (E > kMaxE || k > kMaxK || k > E) return MOE_ERR_UNSUPPORTED;
-    if (int64_t(T) * k >= (int64_t(1) << 31)) return MOE_ERR_OVERFLOW;
+    if (int64_t(T) * k > kMaxPairs) return MOE_ERR_OVERFLOW;
     if (T == 0) return MOE_OK;
     if (!slot_of || !x || !offsets || !active || !out || !aligned16(x) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
     Q4Params p = {};

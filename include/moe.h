@@ -34,7 +34,7 @@
  *    different streams with disjoint outputs.
  *  - Shapes: d and f multiples of 256 (d <= 8192, f <= 8192), 1 <= k <= 16,
  *    k <= E <= 4096, T*k < 2^31. The 4-bit and the unquantised products state
- *    their own N and K.
+ *    their own N and K, and take T*k <= 2^31 - 4096.
  */
 #ifndef MOE_H
 #define MOE_H
@@ -525,8 +525,8 @@ typedef struct moe_q4weights {
  * Codes enter the products exactly and scales apply to sums of a group in fp32,
  * so no weight is rounded. x enters as fp16, each 128 k of a row scaled by a
  * power of two: values down to 2^-25 of the largest of the 128 are exact, smaller
- * ones are rounded at 2^-36 of it. An infinity or a NaN in a row of x makes all
- * of that row's results non-finite. The order of the additions depends on the
+ * ones are rounded at 2^-36 of it (at 2^-120, where the largest is below 2^-86).
+ * An infinity or a NaN in a row of x makes all of that row's results non-finite. The order of the additions depends on the
  * sizes only: equal calls give equal bits.
  * Made for few rows a matrix (decoding, verify batches, small prompts): with
  * more than 8, 16 or 32 of them the codes are read once for each so many rows.
@@ -574,9 +574,9 @@ moe_status moe_expert_linear_q4(const moe_q4weights *W, const int32_t *slot_of, 
  * Rows that belong to no expert are left as they were; dW is written for every
  * expert, also those without rows (T = 0 among them). Sums run in the tensor
  * cores' fp32, rounded once; their order depends on the sizes only. An fp32
- * result of K = 2048 terms is about 1e-6 off (relative, by norms). N and K are multiples of 8 up to 16384, E <= 4096;
- * all tensors but offsets and sorted_tok 16-byte aligned; outputs overlap no
- * input (but base).
+ * result of K = 2048 terms is about 1e-6 off (relative, by norms). N and K are
+ * multiples of 8 up to 16384, E <= 4096; all tensors but offsets and sorted_tok
+ * 16-byte aligned; outputs overlap no input (but base).
  */
 moe_status moe_expert_gemm(const void *a, const void *W, int dtype, int T, int E, int k, int N, int K,
                            const int32_t *offsets, const int32_t *sorted_tok, void *out, int out_dtype,

@@ -44,7 +44,8 @@ def test_q4_refusals():
         assert by_expert(ok, **kw) == INVALID, kw
     for kw in (dict(E=4097), dict(k=17, E=32), dict(k=9)):
         assert by_expert(ok, **kw) == UNSUPPORTED, kw
-    assert by_expert(ok, T=1 << 30) == OVERFLOW
+    assert by_expert(ok, T=1 << 30) == OVERFLOW and by_expert(ok, T=(1 << 31) - 4095, k=1) == OVERFLOW
+    assert dense(ok, T=(1 << 31) - 1) == OVERFLOW
     assert by_expert(ok, T=0, x=None, out=None) == 0
 
 
@@ -77,7 +78,7 @@ def test_gemm_refusals(call):
         assert call(**kw) == INVALID, kw
     for kw in (dict(N=60), dict(K=68), dict(N=16392), dict(K=16392), dict(E=4097), dict(k=17, E=32), dict(k=9)):
         assert call(**kw) == UNSUPPORTED, kw
-    assert call(T=1 << 30) == OVERFLOW
+    assert call(T=1 << 30) == OVERFLOW and call(T=(1 << 31) - 4095, k=1) == OVERFLOW
 
 
 def test_gemm_of_no_tokens():
