@@ -294,3 +294,22 @@ def test_codes_past_32_bit_offsets():
     native.linear_q4(native.q4_weights(codes, scale, None, group), slots - 1, x, 2, out)
     W, mag = dense(codes[slots - 1], scale[slots - 1], None, group)
     assert_close(out, x.double() @ W.t(), (x.double().abs() @ mag.t()) * bound(K, group))
+
+
+def test_far_gate_of_a_large_up_row():
+    """exp(-gate) beyond fp32, the up row large enough for a result near one."""
+    # Gate -8 s x_0 and up 2^14 x_128 are exact. exp is off by two steps of 2^-24 and, at 2^-130 with 2^-149 the
+    # smallest subnormal, by 2^-20; two more roundings: below 2^-19 together.
+    gate_scale = torch.tensor([11.0, 11.0625, 11.125, 11.1875, 11.25, 11.0, 11.125, 11.25])
+    codes = torch.full((64, 128), 0x88, dtype=torch.uint8)
+    codes[:32, 0], codes[32:, 64] = 0x80, 0x89
+    scale = torch.zeros(64, 2)
+    scale[:32, 0], scale[32:, 1] = gate_scale.repeat(4), 2.0 ** 14
+    x = torch.zeros(1, 256, dtype=BF)
+    x[0, 0], x[0, 128] = 1.0, 2.0 ** 112
+    out = torch.empty(1, 32, dtype=F32, device="cuda")
+    native.linear_q4(native.q4_weights(codes.cuda(), scale.half().cuda(), None, 128), 0, x.cuda(), 1, out,
+                     native.ACT_SWIGLU)
+    want = (silu(-8 * gate_scale.double().repeat(4)) * 2.0 ** 126).cuda()[None]
+    assert (want.abs() > 1).all()
+    assert_close(out, want, want.abs() * 2.0 ** -19)
