@@ -1454,13 +1454,16 @@ moe_status launch(DecodeParams p, cudaStream_t stream) {
             return MOE_ERR_CUDA;
         }
         const int av = optin - int(fa.sharedSizeBytes);
-        if (av <= 0 || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, av) != cudaSuccess) {
-            cudaGetLastError();
-            return MOE_ERR_CUDA;
-        }
+        if (av <= 0) return MOE_ERR_CUDA;
         li.sms = sms;
         li.avail = size_t(av);
         li.ready = true;
+    }
+    // on every call: it also makes the device's context current to a host thread
+    // that had none, which the tensor maps' encoder below, a driver call, needs
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(li.avail)) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
     }
     // the format's cluster size, doubled (up to 8) while a task does not fit in shared memory
     int C = cluster_size(FMT, p.d, 8), G = 0;

@@ -902,8 +902,10 @@ bool map_blocks(CUtensorMap *m, bool bf16, const void *base, int64_t inner, int6
     return map16(m, bf16, base, 3, {64, rows, inner / 64, 1}, {1, inner, 64, 0}, {64, 64, 2, 1});
 }
 
-template <typename C>
-moe_status launch(GemmParams &p, const GemmMaps &maps, int64_t most_tiles, int sms, cudaStream_t stream) {
+// encode fills in the tensor maps. It is a driver call, which takes the context
+// that the attribute's call before it has made current to this host thread.
+template <typename C, typename Encode>
+moe_status launch(GemmParams &p, const Encode &encode, int64_t most_tiles, int sms, cudaStream_t stream) {
     p.stages = C::stages(p.E, p.read_base);
     const size_t smem = p.stages * C::kStage + C::fixed(p.E, p.read_base);
     if (cudaFuncSetAttribute(expert_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
@@ -911,13 +913,15 @@ moe_status launch(GemmParams &p, const GemmMaps &maps, int64_t most_tiles, int s
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
+    GemmMaps maps;
+    if (!encode(maps)) return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(sms / C::CG, most_tiles)) * C::CG);
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
-    void *args[] = {&p, const_cast<GemmMaps *>(&maps)};
+    void *args[] = {&p, &maps};
     if (launch_early(cfg, attrs, C::CG, reinterpret_cast<const void *>(expert_gemm_kernel<C>), args) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
@@ -932,7 +936,6 @@ moe_status run_gemm(int pass, GemmParams &p, const void *w, int N, int K, cudaSt
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
-    GemmMaps maps;
     const bool bf = p.bf16, pick = p.sorted_tok != nullptr;
     const int64_t experts = std::min<int64_t>(p.E, p.P);
     // Few rows an expert: the weights' bytes bound the call, so tiles are narrow
@@ -945,40 +948,42 @@ moe_status run_gemm(int pass, GemmParams &p, const void *w, int N, int K, cudaSt
     // One box of two blocks instead of two loads (90 cycles of the issuing
     // thread each), where the extent along MN has no ragged last block.
     p.blocks2 = pass == kWgrad ? N % 64 == 0 && K % 64 == 0 : pass == kDgrad && K % 64 == 0;
-    bool ok = pass == kWgrad ? map_out(&maps.out, bf, p.out_fp32, p.out, K, N, p.E)
-                             : map_out(&maps.out, bf, p.out_fp32, p.out, p.M, p.P, 1);
     p.read_base = p.base && (!p.out_fp32 || p.base != p.out);
-    if (p.read_base) ok = ok && map_out(&maps.base, bf, p.out_fp32, p.base, K, N, p.E);
-    if (p.P > 0) {  // an empty batch (wgrad) has no rows to describe, and loads none
-        if (pass == kForward)
-            ok = ok && map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 128, 1, 1});
-        else if (pass == kDgrad)
-            ok = ok && (p.blocks2
-                            ? map16(&maps.w, bf, w, 4, {64, N, K / 64, p.E}, {1, K, 64, int64_t(N) * K}, {64, 64, 2, 1})
-                            : map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 64, 1, 1}));
-        else
-            ok = ok && (p.blocks2 ? map_blocks(&maps.dy, bf, p.dy, N, p.P) : map_rows(&maps.dy, bf, p.dy, N, p.P, 64));
-        if (!pick && pass == kWgrad)
-            ok = ok && (p.blocks2 ? map_blocks(&maps.rows[0], bf, p.rows, K, p.rows_a)
-                                  : map_rows(&maps.rows[0], bf, p.rows, K, p.rows_a, 64));
-        if (!pick && pass != kWgrad)
-            for (int i = 0; i < (narrow ? 2 : kBoxes); ++i)
-                ok = ok && map_rows(&maps.rows[i], bf, p.rows, p.I, p.rows_a, box_rows(i));
-    }
-    if (!ok) return MOE_ERR_CUDA;
+    auto encode = [&](GemmMaps &maps) {
+        bool ok = pass == kWgrad ? map_out(&maps.out, bf, p.out_fp32, p.out, K, N, p.E)
+                                 : map_out(&maps.out, bf, p.out_fp32, p.out, p.M, p.P, 1);
+        if (p.read_base) ok = ok && map_out(&maps.base, bf, p.out_fp32, p.base, K, N, p.E);
+        if (p.P > 0) {  // an empty batch (wgrad) has no rows to describe, and loads none
+            if (pass == kForward)
+                ok = ok && map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 128, 1, 1});
+            else if (pass == kDgrad)
+                ok = ok && (p.blocks2
+                                ? map16(&maps.w, bf, w, 4, {64, N, K / 64, p.E}, {1, K, 64, int64_t(N) * K}, {64, 64, 2, 1})
+                                : map16(&maps.w, bf, w, 3, {K, N, p.E, 1}, {1, K, int64_t(N) * K, 0}, {64, 64, 1, 1}));
+            else
+                ok = ok && (p.blocks2 ? map_blocks(&maps.dy, bf, p.dy, N, p.P) : map_rows(&maps.dy, bf, p.dy, N, p.P, 64));
+            if (!pick && pass == kWgrad)
+                ok = ok && (p.blocks2 ? map_blocks(&maps.rows[0], bf, p.rows, K, p.rows_a)
+                                      : map_rows(&maps.rows[0], bf, p.rows, K, p.rows_a, 64));
+            if (!pick && pass != kWgrad)
+                for (int i = 0; i < (narrow ? 2 : kBoxes); ++i)
+                    ok = ok && map_rows(&maps.rows[i], bf, p.rows, p.I, p.rows_a, box_rows(i));
+        }
+        return ok;
+    };
     const int64_t MT1 = (p.M + kTileM - 1) / kTileM, MT2 = (MT1 + 1) / 2;
     if (pass == kWgrad)
-        return launch<Cfg<kWgrad, 2, 256, 1>>(p, maps, MT2 * ((N + 255) / 256) * p.E, sms, stream);
+        return launch<Cfg<kWgrad, 2, 256, 1>>(p, encode, MT2 * ((N + 255) / 256) * p.E, sms, stream);
     if (narrow) {
         const int64_t most = MT1 * (experts + p.P / 32);
-        if (pass == kDgrad) return launch<Cfg<kDgrad, 1, 32, 0>>(p, maps, most, sms, stream);
-        return pick ? launch<Cfg<kForward, 1, 32, 2>>(p, maps, most, sms, stream)
-                    : launch<Cfg<kForward, 1, 32, 0>>(p, maps, most, sms, stream);
+        if (pass == kDgrad) return launch<Cfg<kDgrad, 1, 32, 0>>(p, encode, most, sms, stream);
+        return pick ? launch<Cfg<kForward, 1, 32, 2>>(p, encode, most, sms, stream)
+                    : launch<Cfg<kForward, 1, 32, 0>>(p, encode, most, sms, stream);
     }
     const int64_t most = MT2 * (experts + p.P / 256);
-    if (pass == kDgrad) return launch<Cfg<kDgrad, 2, 256, 0>>(p, maps, most, sms, stream);
-    return pick ? launch<Cfg<kForward, 2, 256, 2>>(p, maps, most, sms, stream)
-                : launch<Cfg<kForward, 2, 256, 0>>(p, maps, most, sms, stream);
+    if (pass == kDgrad) return launch<Cfg<kDgrad, 2, 256, 0>>(p, encode, most, sms, stream);
+    return pick ? launch<Cfg<kForward, 2, 256, 2>>(p, encode, most, sms, stream)
+                : launch<Cfg<kForward, 2, 256, 0>>(p, encode, most, sms, stream);
 }
 
 moe_status check_gemm(int dtype, int T, int E, int k, int N, int K, int out_dtype) {
