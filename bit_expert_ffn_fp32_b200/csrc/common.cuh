@@ -48,6 +48,17 @@ inline cudaError_t launch_early(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&a
     cfg.numAttrs = n;
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
+// Dynamic shared memory a launch of fn may ask for: always the template's
+// largest amount, so that calls of several host threads set the same value and
+// none lowers it between another's set and launch. Set on every call, as it
+// belongs to the current device's context.
+template <typename F>
+inline bool allow_smem(F *fn, int most) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
+constexpr int kMaxSmem = 232448;  // of a block, its static shared memory included
 // First thing in such a kernel, by every thread: from here on everything before
 // it on the stream is done and visible; what follows it may be set up as well.
 __device__ __forceinline__ void after_previous() {

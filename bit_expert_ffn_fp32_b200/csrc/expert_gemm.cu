@@ -50,6 +50,7 @@ constexpr int kLoadWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 8, kPickWa
 constexpr int kPickThreads = 128;  // gathering threads that fill a stage
 constexpr int kMaxStages = 10;
 constexpr int kTurn = 2048;      // per epilogue warp: a box of results on its way out
+constexpr int kMaxDynamic = kMaxSmem - 1024;  // 1 KB: GemmSmem
 constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
 
 struct GemmParams {
@@ -106,7 +107,7 @@ struct Cfg {
         return kEpiWarps * kTurn * (1 + read_base) + (size_t(E) + 1) * sizeof(Entry) + 1024;
     }
     static constexpr int stages(int E, int read_base) {
-        const size_t fit = (232448 - 1024 - fixed(E, read_base)) / kStage;  // 1 KB: GemmSmem
+        const size_t fit = (kMaxDynamic - fixed(E, read_base)) / kStage;
         return fit < size_t(kMaxStages) ? int(fit) : kMaxStages;
     }
     // Tensor memory: two buffers, so that the epilogue of one tile runs beside the
@@ -908,11 +909,7 @@ template <typename C, typename Encode>
 moe_status launch(GemmParams &p, const Encode &encode, int64_t most_tiles, int sms, cudaStream_t stream) {
     p.stages = C::stages(p.E, p.read_base);
     const size_t smem = p.stages * C::kStage + C::fixed(p.E, p.read_base);
-    if (cudaFuncSetAttribute(expert_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
-        cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
+    if (!allow_smem(expert_gemm_kernel<C>, kMaxDynamic)) return MOE_ERR_CUDA;
     GemmMaps maps;
     if (!encode(maps)) return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};

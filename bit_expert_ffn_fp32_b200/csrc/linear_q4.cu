@@ -486,12 +486,7 @@ moe_status launch(Q4Params &p, int experts, cudaStream_t stream) {
     p.chunk = std::max(1, std::min(whole, fit)) * unit;
     const size_t smem = size_t(kWarps) * kWarpBytes<G, RG, NB> +
                         size_t(p.chunk) * (per_step + NB * (kStep / G) * 32 + NB * 64);
-    // set on every call: the attribute belongs to the current device's context
-    if (smem > 232448 || cudaFuncSetAttribute(q4_kernel<X, G, RG, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              int(smem)) != cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
+    if (smem > kMaxSmem || !allow_smem(q4_kernel<X, G, RG, NB>, kMaxSmem)) return MOE_ERR_CUDA;
     const int units = p.swiglu ? p.N / 32 : p.N / (16 * RG), per_block = kWarps >> p.ks_log2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((units + per_block - 1) / per_block, experts);
