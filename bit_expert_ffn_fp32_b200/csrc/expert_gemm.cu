@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "row_tiles.h"
 #include "tc05.cuh"
 
 namespace moe {
@@ -135,7 +136,7 @@ __device__ __forceinline__ bool range_of(const GemmParams &p, int e, int &r0, in
 
 template <typename C>
 __device__ __forceinline__ int tiles_of(const GemmParams &p, int rows, int MT) {
-    if (C::PASS != kWgrad) return MT * ((rows + C::TN - 1) / C::TN);
+    if (C::PASS != kWgrad) return MT * row_tiles(rows, C::TN);
     // an expert without rows: nothing to do where the sum so far is in place
     return rows > 0 || p.base != p.out ? MT * ((p.N + C::TN - 1) / C::TN) : 0;
 }
@@ -214,9 +215,8 @@ struct Walk {
         if (C::PASS == kWgrad) {
             t.c0 = j * C::TN;
             t.n = min(C::TN, p.N - t.c0);
-        } else {  // the rows spread evenly over their tiles, in multiples of 16
-            const int nt = (t.rows + C::TN - 1) / C::TN;
-            const int per = nt == 1 ? C::TN : ((t.rows + nt - 1) / nt + 15) & ~15;
+        } else {
+            const int per = rows_per_tile(t.rows, row_tiles(t.rows, C::TN), C::TN);
             t.c0 = t.r0 + j * per;
             t.n = min(per, t.r0 + t.rows - t.c0);
         }
