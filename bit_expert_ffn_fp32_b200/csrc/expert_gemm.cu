@@ -185,7 +185,7 @@ struct Tile {
     int e, m0;       // expert; first M index of this CTA
     int c0, n;       // forward, dgrad: first sorted pair and pairs; wgrad: first n and their number
     int r0, rows;    // the expert's rows
-    int npad, b0;    // n padded to the MMA's 16; first of the npad / CG of them whose B rows this CTA loads
+    int npad, b0;    // n padded to the MMA's 16 a CTA; first of the npad / CG of them whose B rows this CTA loads
 };
 
 // A warp's way through this CTA's tiles.
@@ -221,7 +221,7 @@ struct Walk {
             t.n = min(per, t.r0 + t.rows - t.c0);
         }
         // in 64-wide blocks, each CTA of a pair takes whole ones
-        t.npad = C::PASS == kWgrad && p.blocks2 ? (t.n + 127) & ~127 : (t.n + 15) & ~15;
+        t.npad = C::PASS == kWgrad && p.blocks2 ? (t.n + 127) & ~127 : padded_columns(t.n, C::CG);
         t.b0 = rank * (t.npad / C::CG);
         return t;
     }

@@ -19,4 +19,8 @@ MOE_HD int rows_per_tile(int rows, int tiles, int tn) {
     return tiles == 1 ? tn : ((rows - 1) / tiles + 16) & ~15;
 }
 
+// Columns of the products of n columns by cg CTAs together: an M = 128 product
+// takes multiples of 16, one of M = 256 by a pair of CTAs multiples of 32.
+MOE_HD int padded_columns(int n, int cg) { return (n + 16 * cg - 1) & ~(16 * cg - 1); }
+
 }  // namespace moe

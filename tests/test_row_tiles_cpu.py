@@ -14,6 +14,7 @@ SOURCE = """
 #include "row_tiles.h"
 extern "C" int tiles(int rows, int tn) { return moe::row_tiles(rows, tn); }
 extern "C" int per(int rows, int tn) { return moe::rows_per_tile(rows, moe::row_tiles(rows, tn), tn); }
+extern "C" int columns(int n, int cg) { return moe::padded_columns(n, cg); }
 """
 
 
@@ -36,3 +37,9 @@ def test_rows_are_covered_once(lib, tn):
         assert nt == -(-rows // tn)
         assert 0 < per <= tn and per % 16 == 0
         assert (nt - 1) * per < rows <= nt * per, (rows, nt, per)
+
+
+@pytest.mark.parametrize("cg,unit", [(1, 16), (2, 32)])
+def test_columns_are_what_the_products_take(lib, cg, unit):
+    for n in range(1, 257):
+        assert n <= lib.columns(n, cg) < n + unit and lib.columns(n, cg) % unit == 0
