@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
     int slot = p.slot, r0 = 0, r1 = p.T;
     if (p.slot_of) {
         const int na = p.active[0], e = p.active[1 + blockIdx.y];  // E + 1 entries: blockIdx.y < E
-        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (na < 0 || na > p.E))
+        // more experts than there are pairs (or experts at all): entries that no block looks at
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (na < 0 || na > int(gridDim.y)))
             flag(p.status, MOE_DEV_BAD_INDEX);
         if (int(blockIdx.y) >= na) return;
         if (e < 0 || e >= p.E) {

@@ -544,7 +544,9 @@ moe_status moe_linear_q4(const moe_q4weights *W, int32_t slot, const void *x, in
  *               outside [0,T) sets MOE_DEV_BAD_INDEX and counts as zeros);
  *               sorted_tok NULL: [T*k][K], x_s = x[s]
  *   offsets, active  int32 [E+1] each, from moe_permute; an expert id or a row
- *               range outside its bounds sets MOE_DEV_BAD_INDEX and is skipped
+ *               range outside its bounds sets MOE_DEV_BAD_INDEX and is skipped.
+ *               At most min(E, T*k) experts are active: a larger count sets
+ *               MOE_DEV_BAD_INDEX, and the entries past it are not looked at
  *   out         [T*k][N] or, with MOE_ACT_SWIGLU, [T*k][N/2]
  */
 moe_status moe_expert_linear_q4(const moe_q4weights *W, const int32_t *slot_of, const void *x, int dtype, int T, int E,
