@@ -7,9 +7,9 @@
 // chunks of 8 elements (16-byte loads of every operand, all issued before the
 // first is used), a block 512 chunks in a row; blocks are not persistent, so
 // the loads of one cover the stores of another. sig(g) is formed with the
-// hardware's exp2 and reciprocal: off by about 2^-20 + |g| 2^-24, at most 2^-16
-// where exp still answers, against half a step of 2^-11 (fp16, whose products
-// vanish long before) or 2^-8 in the result.
+// hardware's exp2 and reciprocal: off by about 2^-19 + |g| 2^-23, at most 2^-16,
+// against half a step of 2^-11 (fp16, whose products vanish long before) or 2^-8
+// in the result; backward, gates below -87.3 add a subnormal's 2^-150 to sig(g).
 #include <algorithm>
 
 #include "common.cuh"
@@ -43,14 +43,21 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 1 / (1 + exp(-g)) without an overflow on the way, so that a far gate keeps its
-// share of a large u down to the smallest subnormal: backward for g < 0 as
-// exp(g) / (1 + exp(g)); forward, where three more instructions an element show,
-// with both terms 2^-16 (57.5 against 55.5 us at 81,920 x 768; backward 47.3
-// against 47.7 the other way round).
-template <bool BACKWARD>
+// sig(g) = 1 / (1 + exp(-g)) without an overflow on the way, so that a far gate
+// keeps its share of a large product down to g = -103.97, where sig(g) passes
+// below fp32's smallest subnormal (2^-149) and the result is zero.
+// Forward: g sig(g) u as ((u 2^-16) (2^16 sig(g))) g, with
+//   2^16 sig(g) = 2^-8 / (2^-24 + 2^(-g log2 e - 24)).
+// The divisor stays below 2^126, where the fast division still answers, 2^16
+// sig(g) keeps 15 bits at the far end, and u 2^-16 is exact, for subnormal u too
+// (56.0 us at 81,920 x 768; 55.5 without the scaling of u).
+__device__ __forceinline__ float gated(float g, float u) {
+    const float s = __fdividef(0x1p-8f, 0x1p-24f + exp2_approx(fmaf(g, -1.4426950408889634f, -24.f)));
+    return u * 0x1p-16f * s * g;
+}
+// Backward: for g < 0 as exp(g) / (1 + exp(g)). Below g = -87.3 exp(g) is a
+// subnormal, off by up to 2^-150.
 __device__ __forceinline__ float sigmoid(float g) {
-    if (!BACKWARD) return __fdividef(0x1p-16f, 0x1p-16f + exp2_approx(fmaf(g, -1.4426950408889634f, -16.f)));
     const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e);
     return g < 0.f ? e * r : r;
 }
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const E *gu, const E *
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 gf = Pack2<E>::load(gv[i]), uf = Pack2<E>::load(uv[i]);
-                a[i] = Pack2<E>::store(gf.x * sigmoid<false>(gf.x) * uf.x, gf.y * sigmoid<false>(gf.y) * uf.y);
+                a[i] = Pack2<E>::store(gated(gf.x, uf.x), gated(gf.y, uf.y));
             }
             *reinterpret_cast<uint4 *>(out + w[j].row * f + w[j].col) = make_uint4(a[0], a[1], a[2], a[3]);
         } else {
@@ -106,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const E *gu, const E *
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 gf = Pack2<E>::load(gv[i]), uf = Pack2<E>::load(uv[i]), df = Pack2<E>::load(dv[i]);
-                const float sx = sigmoid<true>(gf.x), sy = sigmoid<true>(gf.y);
+                const float sx = sigmoid(gf.x), sy = sigmoid(gf.y);
                 a[i] = Pack2<E>::store(df.x * uf.x * sx * (1.0f + gf.x * (1.0f - sx)),
                                        df.y * uf.y * sy * (1.0f + gf.y * (1.0f - sy)));
                 b[i] = Pack2<E>::store(df.x * gf.x * sx, df.y * gf.y * sy);

@@ -597,7 +597,10 @@ moe_status moe_expert_gemm_wgrad(const void *dy, const void *a, int dtype, int T
  *   moe_swiglu           h = silu(g) * u                              [rows][f]
  *   moe_swiglu_backward  dg = dh * u * sig(g) * (1 + g * (1 - sig(g))),
  *                        du = dh * silu(g)                     dgu [rows][2f]
- * in fp32, rounded once. f is a multiple of 8; all tensors 16-byte aligned.
+ * in fp32, rounded once. sig(g) below fp32's smallest subnormal (g < -103.97)
+ * is zero; backward it is held as a subnormal below g = -87.3, so that results
+ * of such gates, if a large product brings them back, have its few digits.
+ * f is a multiple of 8 up to 16384, rows < 2^31; all tensors 16-byte aligned.
  * dgu may be gu itself; otherwise outputs overlap no input.
  */
 moe_status moe_swiglu(const void *gu, int dtype, int64_t rows, int f, void *h, moe_stream_t stream);
