@@ -466,9 +466,12 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
                 y += part[row];
                 if (RG == 2 && p.swiglu) up += part[16 + row];
             }
-            if (RG == 2 && p.swiglu) {  // e^-|y|: a far gate keeps its share of a large up row
-                const float e = expf(-fabsf(y));
-                y = (y < 0.f ? y * e : y) / (1.0f + e) * up;
+            if (RG == 2 && p.swiglu) {
+                // e^(-|y|/2), once for the gate and once for the up row: neither is a subnormal where their product
+                // is not, so a far gate keeps its share of a large up row, and its digits
+                const float e = expf(-0.5f * fabsf(y));
+                if (y < 0.f) y *= e, up *= e;
+                y = y / (1.0f + e * e) * up;
             }
             const int64_t at = int64_t(pass + tok) * cols + unit0 * per_unit + c;
             if (p.out_fp32) static_cast<float *>(p.out)[at] = y;
