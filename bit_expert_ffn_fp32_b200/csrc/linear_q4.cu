@@ -10,13 +10,19 @@
 // tokens as the columns), and what limits them is instructions: 8 codes of a
 // word must take few. A code masked where it stands is the fp16 subnormal
 // q * 2^-24 (bits 0-3 of a half) or q * 2^-20 (bits 4-7), exactly, so a word
-// costs four masks and one shift. x enters as fp16: 128 k of a token are scaled
+// costs four masks and one shift. Without min the operand is q - 8 itself: one
+// half-pair FMA, exact too, makes (q - 8) * 2^-9 or 2^-5 of it. Four instructions
+// more a word (8192 x 8192, one token: 12.1 -> 12.6 us; four tokens' down rows
+// 18.1 -> 19.2; with 1024 + q and 64 + q and a subtraction 15.0 and 19.5), but q x
+// and 8 x apart would cancel: an outlier on a zero weight would take the digits
+// of every other product. x enters as fp16: 128 k of a token are scaled
 // by a power of two that brings their largest to [2^14, 2^15), and the k of the
 // codes at 2^-20 by another 2^-4. bf16 and fp16 values stay exact down to 2^-25
 // of the largest; below that they are rounded at 2^-36 of it, under the 2^-24
 // of the fp32 sums they join. No weight is rounded; in fp32, by group and then
 // by 128 k:
-//   sum_k w x = 2^-e * (s * 2^24 * sum (q 2^-24) (x 2^e) + m * sum x 2^e)   (m = -8 s without min)
+//   sum_k w x = 2^-e * (s * 2^24 * sum (q 2^-24) (x 2^e) + m * sum x 2^e)   with min
+//             = 2^-e * s * 2^9 * sum ((q - 8) 2^-9) (x 2^e)                 without
 // An infinity or a NaN in x makes its row's results non-finite, all of them.
 #include <algorithm>
 
@@ -48,14 +54,27 @@ struct Q4Params {
     int32_t *status;
 };
 
+__device__ __forceinline__ uint32_t fma_halves(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
 // The four half pairs of a code word as fp16: codes (0, 4) and (2, 6) times
-// 2^-24, codes (1, 5) and (3, 7) times 2^-20.
+// 2^-24, codes (1, 5) and (3, 7) times 2^-20; without min, the codes less 8,
+// times 2^-9 and 2^-5.
+template <bool MIN>
 __device__ __forceinline__ void halves_of(uint32_t w, uint32_t (&h)[4]) {
     const uint32_t v = w >> 8;
     h[0] = w & 0x000F000Fu;
     h[1] = w & 0x00F000F0u;
     h[2] = v & 0x000F000Fu;
     h[3] = v & 0x00F000F0u;
+    if constexpr (!MIN) {  // times 2^15, less 8
+        h[0] = fma_halves(h[0], 0x78007800u, 0xA400A400u);  // -8 * 2^-9
+        h[1] = fma_halves(h[1], 0x78007800u, 0xB400B400u);  // -8 * 2^-5
+        h[2] = fma_halves(h[2], 0x78007800u, 0xA400A400u);
+        h[3] = fma_halves(h[3], 0x78007800u, 0xB400B400u);
+    }
 }
 __device__ __forceinline__ void mma_fp16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -114,8 +133,9 @@ __device__ __forceinline__ float half_at(const uint4 &v, int j) {
 
 // Grid: (row blocks, active experts or 1). X: type of x; G: group; RG: 16-row
 // groups a warp owns (2: 32 rows, or with SwiGLU 16 gate rows and their 16 up
-// rows); NB: tiles of 8 tokens whose sums a warp keeps.
-template <typename X, int G, int RG, int NB>
+// rows); NB: tiles of 8 tokens whose sums a warp keeps; MIN: weights have
+// an offset.
+template <typename X, int G, int RG, int NB, bool MIN>
 __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const __grid_constant__ Q4Params p) {
     after_previous();
     constexpr int R = 16 * RG, W = G / 32, J = kStep / G;
@@ -159,12 +179,12 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
     const uint32_t ring = tc::smem_u32(mine);
     float4 *pairs = reinterpret_cast<float4 *>(mine + kRingBytes<RG, NB>);  // [J][RG][8]: {s, c} of rows g and g + 8
     // x of a chunk of k, 16 bytes (8 k) of one token each: [tile][step][32 units][tokens], a step's units in the order
-    // (group, code word of a lane, lane t); then the sums of the scaled x:
+    // (group, code word of a lane, lane t); then, with min, the sums of the scaled x:
     // [tile][group][8 tokens]
     const int tile_units = p.chunk * (kStep / 8) << p.ts_log2;
     uint4 *xs = reinterpret_cast<uint4 *>(smem + kWarps * kWarpBytes<G, RG, NB>);
     float *xsum = reinterpret_cast<float *>(xs + NB * tile_units);
-    float *xdown = xsum + NB * p.chunk * J * 8;  // 2^-e: [tile][128 k][8 tokens]
+    float *xdown = xsum + (MIN ? NB * p.chunk * J * 8 : 0);  // 2^-e: [tile][128 k][8 tokens]
     // this lane's 16-byte parts of a step: parts t and t + 4 of rows g + 8i
     const uint8_t *src[2 * RG];
 #pragma unroll
@@ -175,7 +195,7 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
     {
         const int64_t row = slot_row + (busy ? weight_row(lane & (R - 1)) : 0);
         srow = p.scale + row * groups;
-        mrow = p.min ? p.min + row * groups : nullptr;
+        if constexpr (MIN) mrow = p.min + row * groups;
     }
     auto issue = [&](int step, int stage) {
         if (busy && step < steps) {
@@ -203,7 +223,7 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
     auto issue_scales = [&](int step, uint4 &s, uint4 &m) {
         if (busy && step < steps) {
             s = load_scales<G>(srow, step * J, groups, p.scales_in_words);
-            if (mrow) m = load_scales<G>(mrow, step * J, groups, p.scales_in_words);
+            if constexpr (MIN) m = load_scales<G>(mrow, step * J, groups, p.scales_in_words);
         }
     };
 
@@ -288,11 +308,11 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
                     }
                     part += eight;
                 }
-                if (G >= 64) part += __shfl_xor_sync(0xffffffffu, part, TS);
-                if (G >= 128) part += __shfl_xor_sync(0xffffffffu, part, 2 * TS);
+                if (MIN && G >= 64) part += __shfl_xor_sync(0xffffffffu, part, TS);
+                if (MIN && G >= 128) part += __shfl_xor_sync(0xffffffffu, part, 2 * TS);
                 if (nb < tiles && quad < quads) {
                     const int slot8 = i & (TS - 1);
-                    if ((quad & (G / 32 - 1)) == 0) xsum[(nb * cgroups + quad / (G / 32)) * 8 + slot8] = part;
+                    if (MIN && (quad & (G / 32 - 1)) == 0) xsum[(nb * cgroups + quad / (G / 32)) * 8 + slot8] = part;
                     if ((quad & 3) == 0)
                         xdown[(nb * p.chunk * 2 + quad / 4) * 8 + slot8] = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
@@ -323,7 +343,7 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
 #pragma unroll
                             for (int j = 0; j < J; ++j) {
                                 const float s = half_at(sc[d], j);
-                                own[j * R] = make_float2(s * 16777216.f, p.min ? half_at(mn[d], j) : -8.f * s);
+                                own[j * R] = MIN ? make_float2(s * 16777216.f, half_at(mn[d], j)) : make_float2(s * 512.f, 0.f);
                             }
                         }
                         __syncwarp();
@@ -362,8 +382,8 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
                                 uint32_t lo[RG][4], hi[RG][4];
 #pragma unroll
                                 for (int rg = 0; rg < RG; ++rg) {
-                                    halves_of(w[rg][0][wi], lo[rg]);
-                                    halves_of(w[rg][1][wi], hi[rg]);
+                                    halves_of<MIN>(w[rg][0][wi], lo[rg]);
+                                    halves_of<MIN>(w[rg][1][wi], hi[rg]);
                                 }
 #pragma unroll
                                 for (int nb = 0; nb < NB; ++nb) {
@@ -379,21 +399,27 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
                             float2 x01[NB];
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb)
-                                if (NB == 1 || nb < tiles)
+                                if (MIN && (NB == 1 || nb < tiles))
                                     x01[nb] = *reinterpret_cast<const float2 *>(
                                         xsum + (nb * cgroups + (step - c0) * J + j) * 8 + 2 * t);
 #pragma unroll
                             for (int rg = 0; rg < RG; ++rg) {
-                                const float4 f = pairs[(j * RG + rg) * 8 + g];  // s 2^24, m of row g, then of row g + 8
+                                const float4 f = pairs[(j * RG + rg) * 8 + g];  // s 2^24, m (s 2^9, 0) of row g, then of row g + 8
 #pragma unroll
                                 for (int nb = 0; nb < NB; ++nb) {
                                     if (NB > 1 && nb >= tiles) break;
                                     float(&o)[4] = y[nb][rg];
                                     const float(&v)[4] = acc[nb][rg];
-                                    o[0] = fmaf(f.x, v[0], fmaf(f.y, x01[nb].x, o[0]));
-                                    o[1] = fmaf(f.x, v[1], fmaf(f.y, x01[nb].y, o[1]));
-                                    o[2] = fmaf(f.z, v[2], fmaf(f.w, x01[nb].x, o[2]));
-                                    o[3] = fmaf(f.z, v[3], fmaf(f.w, x01[nb].y, o[3]));
+                                    if constexpr (MIN) {
+                                        o[0] = fmaf(f.y, x01[nb].x, o[0]);
+                                        o[1] = fmaf(f.y, x01[nb].y, o[1]);
+                                        o[2] = fmaf(f.w, x01[nb].x, o[2]);
+                                        o[3] = fmaf(f.w, x01[nb].y, o[3]);
+                                    }
+                                    o[0] = fmaf(f.x, v[0], o[0]);
+                                    o[1] = fmaf(f.x, v[1], o[1]);
+                                    o[2] = fmaf(f.z, v[2], o[2]);
+                                    o[3] = fmaf(f.z, v[3], o[3]);
                                 }
                             }
                         };
@@ -481,7 +507,7 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 4 ? 1 : 2) q4_kernel(const 
     }
 }
 
-template <typename X, int G, int RG, int NB>
+template <typename X, int G, int RG, int NB, bool MIN>
 moe_status launch(Q4Params &p, int experts, cudaStream_t stream) {
     // x of the whole of k where two blocks of an SM still fit (one, with more
     // tiles of tokens), else in chunks
@@ -489,8 +515,8 @@ moe_status launch(Q4Params &p, int experts, cudaStream_t stream) {
     const int whole = (steps + unit - 1) / unit, fit = (NB == 1 ? 36 : 128) * 1024 / (per_step * unit);
     p.chunk = std::max(1, std::min(whole, fit)) * unit;
     const size_t smem = size_t(kWarps) * kWarpBytes<G, RG, NB> +
-                        size_t(p.chunk) * (per_step + NB * (kStep / G) * 32 + NB * 64);
-    if (smem > kMaxSmem || !allow_smem(q4_kernel<X, G, RG, NB>, kMaxSmem)) return MOE_ERR_CUDA;
+                        size_t(p.chunk) * (per_step + (MIN ? NB * (kStep / G) * 32 : 0) + NB * 64);
+    if (smem > kMaxSmem || !allow_smem(q4_kernel<X, G, RG, NB, MIN>, kMaxSmem)) return MOE_ERR_CUDA;
     const int units = p.swiglu ? p.N / 32 : p.N / (16 * RG), per_block = kWarps >> p.ks_log2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((units + per_block - 1) / per_block, experts);
@@ -499,27 +525,29 @@ moe_status launch(Q4Params &p, int experts, cudaStream_t stream) {
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
     void *args[] = {&p};
-    if (launch_early(cfg, attrs, 1, reinterpret_cast<const void *>(q4_kernel<X, G, RG, NB>), args) != cudaSuccess) {
+    if (launch_early(cfg, attrs, 1, reinterpret_cast<const void *>(q4_kernel<X, G, RG, NB, MIN>), args) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
     return MOE_OK;
 }
 
-template <typename X, int G>
+template <typename X, int G, bool MIN>
 moe_status launch_g(Q4Params &p, int rg, int nb, int experts, cudaStream_t stream) {
     if (rg == 1)
-        return nb == 1 ? launch<X, G, 1, 1>(p, experts, stream)
-                       : nb == 2 ? launch<X, G, 1, 2>(p, experts, stream) : launch<X, G, 1, 4>(p, experts, stream);
-    return nb == 1 ? launch<X, G, 2, 1>(p, experts, stream)
-                   : nb == 2 ? launch<X, G, 2, 2>(p, experts, stream) : launch<X, G, 2, 4>(p, experts, stream);
+        return nb == 1 ? launch<X, G, 1, 1, MIN>(p, experts, stream)
+                       : nb == 2 ? launch<X, G, 1, 2, MIN>(p, experts, stream)
+                                 : launch<X, G, 1, 4, MIN>(p, experts, stream);
+    return nb == 1 ? launch<X, G, 2, 1, MIN>(p, experts, stream)
+                   : nb == 2 ? launch<X, G, 2, 2, MIN>(p, experts, stream)
+                             : launch<X, G, 2, 4, MIN>(p, experts, stream);
 }
 
-template <typename X>
+template <typename X, bool MIN>
 moe_status launch_x(Q4Params &p, int group, int rg, int nb, int experts, cudaStream_t stream) {
-    return group == 32 ? launch_g<X, 32>(p, rg, nb, experts, stream)
-                       : group == 64 ? launch_g<X, 64>(p, rg, nb, experts, stream)
-                                     : launch_g<X, 128>(p, rg, nb, experts, stream);
+    return group == 32 ? launch_g<X, 32, MIN>(p, rg, nb, experts, stream)
+                       : group == 64 ? launch_g<X, 64, MIN>(p, rg, nb, experts, stream)
+                                     : launch_g<X, 128, MIN>(p, rg, nb, experts, stream);
 }
 
 moe_status run_q4(const moe_q4weights *W, Q4Params &p, const void *x, int dtype, int act, void *out, int out_dtype,
@@ -560,8 +588,11 @@ moe_status run_q4(const moe_q4weights *W, Q4Params &p, const void *x, int dtype,
     if (!p.swiglu && (units << (ks + 1)) <= slots) rg = 1;
     if (units > slots && steps >= 8) ks = 1;
     p.ks_log2 = ks;
-    return dtype == MOE_BF16 ? launch_x<__nv_bfloat16>(p, W->group, rg, nb, experts, stream)
-                             : launch_x<__half>(p, W->group, rg, nb, experts, stream);
+    if (dtype == MOE_BF16)
+        return W->min ? launch_x<__nv_bfloat16, true>(p, W->group, rg, nb, experts, stream)
+                      : launch_x<__nv_bfloat16, false>(p, W->group, rg, nb, experts, stream);
+    return W->min ? launch_x<__half, true>(p, W->group, rg, nb, experts, stream)
+                  : launch_x<__half, false>(p, W->group, rg, nb, experts, stream);
 }
 
 moe_status check_q4(const moe_q4weights *W, int dtype, int act, int out_dtype) {

@@ -522,8 +522,10 @@ typedef struct moe_q4weights {
  * out[t] = W[slot] x[t] for T rows x (a projection next to the layer).
  *   x    bf16 or fp16 [T][K] (dtype), 16-byte aligned
  *   out  [T][N], with MOE_ACT_SWIGLU [T][N/2], in out_dtype: x's type or MOE_FP32
- * Codes enter the products exactly and scales apply to sums of a group in fp32,
- * so no weight is rounded. x enters as fp16, each 128 k of a row scaled by a
+ * Codes (without min: q - 8) enter the products exactly and scales apply to sums
+ * of a group in fp32, so no weight is rounded; with min, s*q and m meet only as
+ * sums of a group, and where they cancel (a far larger x at a weight near zero),
+ * what is left has fp32's digits of either. x enters as fp16, each 128 k of a row scaled by a
  * power of two: values down to 2^-25 of the largest of the 128 are exact, smaller
  * ones are rounded at 2^-36 of it (at 2^-120, where the largest is below 2^-86).
  * An infinity or a NaN in a row of x makes all of that row's results non-finite. The order of the additions depends on the
