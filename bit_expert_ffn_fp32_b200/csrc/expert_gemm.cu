@@ -66,7 +66,6 @@ struct GemmParams {
     int bf16, out_fp32;
     int stages;      // of the shared-memory ring
     int read_base;   // 1: wgrad's sum so far is read (0: there is none, or the results are added where it is)
-    int split;       // 1: an fp32 result is summed in several accumulators
     int blocks2;     // 1: MN-major operands are mapped in 64-wide blocks, two a box (extents multiples of 64)
     int32_t *status;
 };
@@ -112,11 +111,11 @@ struct Cfg {
         return fit < size_t(kMaxStages) ? int(fit) : kMaxStages;
     }
     // Tensor memory: two buffers, so that the epilogue of one tile runs beside the
-    // products of the next. An fp32 result of a long sum is formed in kAccs
-    // accumulators, its stages in turn, added at the end: the tensor cores cut
-    // instead of round, an error that grows with the length of a chain. Narrow
-    // tiles have room for four in each buffer; wide ones take both buffers.
-    static constexpr int kAccs = CG == 1 ? 4 : 2, kBuf = CG == 1 ? kAccs * TN : TN, kCols = 2 * kBuf;
+    // products of the next. The tensor cores cut instead of round, an error that
+    // grows with the length of a chain: narrow tiles with fp32 results take the
+    // stages of a buffer in turns to kAccs accumulators, added at the end, and a
+    // tile whose sums are long takes both buffers (segments_of).
+    static constexpr int kAccs = CG == 1 ? 4 : 1, kBuf = kAccs * TN, kCols = 2 * kBuf;
     static_assert(stages(kMaxE, PASS == kWgrad) >= 4 && sizeof(GemmSmem) <= 1024 && kCols >= 32 && kCols <= 512,
                   "tile does not fit");
 };
@@ -232,13 +231,46 @@ __device__ __forceinline__ int stages_of(const GemmParams &p, const Tile &t) {
     return ((C::PASS == kWgrad ? t.rows : p.I) + kTileI - 1) / kTileI;
 }
 
-// Accumulator buffer, and the phase of its barriers, of a CTA's tile number count.
+// A tile's stages fall into segments, so that no chain of an fp32 result is
+// longer than 1024 products of the contracted index (relative error 1e-6 by
+// norms; 9e-6 at 16384 in two chains; wide tiles keep to one of 768, 7e-7, or two
+// up to 2048), none of a 16-bit one longer than 16384 (1.5e-5, against half a
+// step of 4.9e-4 in fp16). One segment: a buffer, the
+// tiles take them in turns. Several: the first is summed in the tile's buffer,
+// the others in the other one, from where the epilogue adds them to the first;
+// each costs the tensor cores a pause of the epilogue's two reads and a write
+// (fp32 results of 8 x 512 rows, N = 2048, in a burst: K = 4096 60.2 -> 62.2 us,
+// 16384 213 -> 226; 2048 34.6 -> 34.8).
+struct Segments {
+    int count, per;  // per: stages of each but the last
+};
 template <typename C>
-__device__ __forceinline__ int buffer_of(const GemmParams &p, int count, uint32_t &phase) {
-    const bool one = C::CG == 2 && p.split;
-    phase = (one ? count : count >> 1) & 1;
-    return one ? 0 : count & 1;
+__device__ __forceinline__ Segments segments_of(const GemmParams &p, int KS) {
+    const int most = p.out_fp32 ? 16 * C::kAccs : 256;
+    const int least = C::kAccs == 1 && p.out_fp32 && KS > 12 ? 2 : 1, count = max(least, (KS + most - 1) / most);
+    return {count, (KS + count - 1) / count};
 }
+// Accumulators of a buffer that a segment of `stages` fills.
+template <typename C>
+__device__ __forceinline__ int accs_of(const GemmParams &p, int stages) {
+    return p.out_fp32 ? min(C::kAccs, stages) : min(1, stages);
+}
+
+// The buffers as a role goes through them: whose turn it is, and the phase of
+// each buffer's barriers.
+struct Buffers {
+    int next = 0;
+    uint32_t phases = 0;
+    // The buffer of segment i of a tile, and its phase.
+    __device__ __forceinline__ int take(int i, uint32_t &phase) {
+        const int b = next ^ int(i > 0);
+        phase = (phases >> b) & 1;
+        phases ^= 1u << b;
+        return b;
+    }
+    // After a tile: one with several segments leaves the other buffer last.
+    __device__ __forceinline__ void turn(const Segments &g) { next ^= int(g.count == 1); }
+};
 
 // MN-major operand, 128-byte swizzle: blocks of 64 along MN 8192 bytes apart
 // (leading offset), groups of 8 along the contracted index 1024 bytes apart.
@@ -494,47 +526,51 @@ __device__ void issue_mma(const GemmParams &p, GemmSmem &s, unsigned char *dyn, 
         else tc::mma_commit(bar);
     };
     Ring at(p.stages);
-    int count = 0;
+    Buffers bufs;
     bool ok = true;
     for (int tau = blockIdx.x / C::CG; tau < total && ok && !s.abort; tau += gridDim.x / C::CG) {
         const Tile t = walk.tile(p, tau);
         const int KS = stages_of<C>(p, t);
         if (KS == 0) continue;  // wgrad of an expert without rows
-        uint32_t phase;
-        const int buf = buffer_of<C>(p, count, phase);
-        if (!tc::mbar_wait_warp(&s.tempty[buf], phase ^ 1, kWaitNs)) {
-            ok = false;
-            break;
-        }
-        tc::fence_after();
-        ++count;
+        const Segments segs = segments_of<C>(p, KS);
         const uint32_t idesc = idesc0 | (uint32_t(t.npad >> 3) << 17);
-        const uint32_t d0 = tmem + uint32_t(buf * C::kBuf);
-        const int accs = p.split ? C::kAccs : 1;
+        const int accs = p.out_fp32 ? C::kAccs : 1;
         int left = C::PASS == kWgrad ? t.rows : p.I;
-        for (int ks = 0; ks < KS; ++ks, left -= kTileI, at.next()) {
-            if (!tc::mbar_wait_warp(&s.full[at.stage], at.phase, kWaitNs)) {
+        for (int seg = 0; seg < segs.count && ok; ++seg) {
+            uint32_t phase;
+            const int buf = bufs.take(seg, phase), here = min(segs.per, KS - seg * segs.per);
+            if (!tc::mbar_wait_warp(&s.tempty[buf], phase ^ 1, kWaitNs)) {
                 ok = false;
                 break;
             }
             tc::fence_after();
-            const uint64_t a = a0 + uint32_t(at.stage * (C::kStage >> 4)), b = b0 + uint32_t(at.stage * (C::kStage >> 4));
-            const uint32_t d = d0 + uint32_t((ks & (accs - 1)) * C::TN);
-            if (tc::elect_one()) {
-                mma(d, a, b, idesc, ks >= accs ? 1u : 0u);
-                if (left > 48) {
-                    mma(d, a + kStepA, b + kStepB, idesc, 1u);
-                    mma(d, a + 2 * kStepA, b + 2 * kStepB, idesc, 1u);
-                    mma(d, a + 3 * kStepA, b + 3 * kStepB, idesc, 1u);
-                } else {  // steps of 16; the last one reads zeros past the end
-                    if (left > 16) mma(d, a + kStepA, b + kStepB, idesc, 1u);
-                    if (left > 32) mma(d, a + 2 * kStepA, b + 2 * kStepB, idesc, 1u);
+            const uint32_t d0 = tmem + uint32_t(buf * C::kBuf);
+            for (int ks = 0; ks < here; ++ks, left -= kTileI, at.next()) {
+                if (!tc::mbar_wait_warp(&s.full[at.stage], at.phase, kWaitNs)) {
+                    ok = false;
+                    break;
                 }
-                commit(&s.empty[at.stage]);
-                if (ks == KS - 1) commit(&s.tfull[buf]);
+                tc::fence_after();
+                const uint64_t a = a0 + uint32_t(at.stage * (C::kStage >> 4)),
+                               b = b0 + uint32_t(at.stage * (C::kStage >> 4));
+                const uint32_t d = d0 + uint32_t((ks & (accs - 1)) * C::TN);
+                if (tc::elect_one()) {
+                    mma(d, a, b, idesc, ks >= accs ? 1u : 0u);
+                    if (left > 48) {
+                        mma(d, a + kStepA, b + kStepB, idesc, 1u);
+                        mma(d, a + 2 * kStepA, b + 2 * kStepB, idesc, 1u);
+                        mma(d, a + 3 * kStepA, b + 3 * kStepB, idesc, 1u);
+                    } else {  // steps of 16; the last one reads zeros past the end
+                        if (left > 16) mma(d, a + kStepA, b + kStepB, idesc, 1u);
+                        if (left > 32) mma(d, a + 2 * kStepA, b + 2 * kStepB, idesc, 1u);
+                    }
+                    commit(&s.empty[at.stage]);
+                    if (ks == here - 1) commit(&s.tfull[buf]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
+        bufs.turn(segs);
     }
     if (!ok) stop(s, p.status);
 }
@@ -665,9 +701,10 @@ __device__ __forceinline__ bool store_tile16(const GemmParams &p, const Out &to,
     return ok;
 }
 
-// 32 columns of fp32, the sum of `accs` accumulators (none: zeros).
+// 32 columns of fp32, the sum of `accs` accumulators at td (none: zeros) and of
+// `more` at td2.
 template <typename C>
-__device__ __forceinline__ void fetch32(uint32_t td, int accs, uint32_t (&v)[32]) {
+__device__ __forceinline__ void fetch32(uint32_t td, int accs, uint32_t td2, int more, uint32_t (&v)[32]) {
     if (accs == 0) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = 0u;
@@ -675,25 +712,48 @@ __device__ __forceinline__ void fetch32(uint32_t td, int accs, uint32_t (&v)[32]
     }
     tc::tmem_ld32_nowait(td, v);
     tc::tmem_ld_wait();
-    for (int a = 1; a < accs; ++a) {
-        uint32_t u[32];
-        tc::tmem_ld32_nowait(td + uint32_t(a * C::TN), u);
-        tc::tmem_ld_wait();
+    for (int a = 1; a < accs + more; ++a) {
+        const uint32_t from = a < accs ? td + uint32_t(a * C::TN) : td2 + uint32_t((a - accs) * C::TN);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+        for (int h = 0; h < 32; h += 16) {
+            uint32_t u[16];
+            tc::tmem_ld16_nowait(from + h, u);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[h + i] = __float_as_uint(__uint_as_float(v[h + i]) + __uint_as_float(u[i]));
+        }
     }
+}
+
+// Adds this warp's values of the `accs` accumulators at from to those at td, in
+// tensor memory, rounding to nearest.
+template <typename C>
+__device__ __forceinline__ void add_segment(uint32_t td, uint32_t from, int accs, int n, int half) {
+    for (int a = 0; a < accs; ++a)
+        for (int c = a * C::TN + 32 * half; c < a * C::TN + n; c += 64)
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+                uint32_t v[16], u[16];
+                tc::tmem_ld16_nowait(td + c + h, v);
+                tc::tmem_ld16_nowait(from + c + h, u);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+                tc::tmem_st16(td + c + h, v);
+            }
+    tc::tmem_st_wait();
 }
 
 // fp32 results, [column][32], 16 columns at a time.
 template <typename C, bool ADD>
 __device__ __forceinline__ bool store_tile32(const GemmParams &p, const Out &to, uint32_t &based, const Tile &t,
-                                             int accs, uint32_t td, int half, int m1) {
+                                             int accs, uint32_t td, int more, uint32_t td2, int half, int m1) {
     const int lane = threadIdx.x & 31, m = m1 + lane;
     bool ok = true;
     float *o = static_cast<float *>(p.out) + int64_t(t.c0) * p.M + m;
     for (int c = 32 * half; c < t.n; c += 64) {
         uint32_t v[32];
-        fetch32<C>(td + c, accs, v);
+        fetch32<C>(td + c, accs, td2 + c, more, v);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int c1 = c + 16 * h;
@@ -735,39 +795,63 @@ __device__ void store_tiles(const GemmParams &p, GemmSmem &s, const GemmMaps &ma
     const uint32_t turn = tc::smem_u32(dyn) + p.stages * C::kStage + warp * kTurn;
     const Out to = {&maps.out, &maps.base, &s.based[warp], turn, turn + kEpiWarps * kTurn};
     uint32_t based = 0;
-    int count = 0;
+    Buffers bufs;
     for (int tau = blockIdx.x / C::CG; tau < total && !s.abort; tau += gridDim.x / C::CG) {
         const Tile t = walk.tile(p, tau);
-        const int KS = stages_of<C>(p, t), accs = p.split ? min(C::kAccs, KS) : min(1, KS);  // 0: no sums
-        uint32_t phase;
-        const int m1 = t.m0 + 32 * q, buf = buffer_of<C>(p, count, phase);
+        const int KS = stages_of<C>(p, t);
+        // (forward's and dgrad's 16-bit results: N and K stop at 16384)
+        constexpr bool kMany = sizeof(O) == 4 || C::PASS == kWgrad;
+        const Segments segs = kMany ? segments_of<C>(p, KS) : Segments{1, KS};
+        const int m1 = t.m0 + 32 * q;
         const bool any = m1 < p.M && 32 * half < t.n;  // of this warp's values lie in the result
         if (ADD && any) to.want(t, m1, 32 * half);
-        bool ok = true;
-        if (accs) {
-            // a tile of many stages may rightly take longer than one wait
-            ok = tc::mbar_wait_warp(&s.tfull[buf], phase, kWaitNs + 2000ull * KS);
+        const uint32_t quad = tmem + (uint32_t(32 * q) << 16);
+        auto filled = [&](int b, uint32_t phase) {
+            // a segment of many stages may rightly take longer than one wait
+            const bool ok = tc::mbar_wait_warp(&s.tfull[b], phase, kWaitNs + 2000ull * segs.per);
             tc::fence_after();
-            ++count;
+            return ok;
+        };
+        auto release = [&](int b) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t bar = tc::smem_u32(&s.tempty[b]);
+                tc::mbar_arrive_cluster(C::CG == 2 ? tc::at_rank(bar, 0) : bar);
+            }
+        };
+        bool ok = true;
+        int buf = 0, last = 0, accs = 0, more = 0;  // more: accumulators of the last segment, still in their buffer
+        if (KS > 0) {
+            uint32_t phase;
+            buf = bufs.take(0, phase);
+            accs = accs_of<C>(p, segs.per);
+            ok = filled(buf, phase);
+            for (int seg = 1; kMany && seg < segs.count && ok; ++seg) {
+                last = bufs.take(seg, phase);
+                ok = filled(last, phase);
+                const int here = accs_of<C>(p, min(segs.per, KS - seg * segs.per));
+                if (sizeof(O) == 4 && seg == segs.count - 1) {
+                    more = here;
+                } else {
+                    if (ok && any) add_segment<C>(quad + buf * C::kBuf, quad + last * C::kBuf, here, t.n, half);
+                    release(last);
+                }
+            }
+            bufs.turn(segs);
         }
-        const uint32_t td = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf * C::kBuf);
+        const uint32_t td = quad + uint32_t(buf * C::kBuf), td2 = quad + uint32_t(last * C::kBuf);
         if (ok && any) {
             if constexpr (sizeof(O) == 2) ok = store_tile16<C, O, ADD>(p, to, based, t, accs > 0, td, half, m1);
-            else ok = store_tile32<C, ADD>(p, to, based, t, accs, td, half, m1);
+            else ok = store_tile32<C, ADD>(p, to, based, t, accs, td, more, td2, half, m1);
         }
         if (!ok) {  // no box may land after this CTA's shared memory has another owner
             stop(s, p.status);
             if (ADD && any) to.got(based);
             break;
         }
-        if (accs) {
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                const uint32_t bar = tc::smem_u32(&s.tempty[buf]);
-                tc::mbar_arrive_cluster(C::CG == 2 ? tc::at_rank(bar, 0) : bar);
-            }
-        }
+        if (accs) release(buf);
+        if (more) release(last);
     }
     if (lane == 0) tc::bulk_wait_read<0>();
 }
@@ -938,10 +1022,6 @@ moe_status run_gemm(int pass, GemmParams &p, const void *w, int N, int K, cudaSt
     // Few rows an expert: the weights' bytes bound the call, so tiles are narrow
     // and single, with more stages of weights in flight and more of them.
     const bool narrow = pass != kWgrad && p.P <= 16 * experts;
-    // Chains of more than 768: relative error 7e-7 there, where fp32 products summed
-    // in fp32 have 2e-7. (wgrad: by the rows an expert has on average.)
-    const int64_t chain = pass == kWgrad ? p.P / std::max<int64_t>(experts, 1) : p.I;
-    p.split = p.out_fp32 && (narrow || chain > 768);
     // One box of two blocks instead of two loads (90 cycles of the issuing
     // thread each), where the extent along MN has no ragged last block.
     p.blocks2 = pass == kWgrad ? N % 64 == 0 && K % 64 == 0 : pass == kDgrad && K % 64 == 0;
@@ -1004,7 +1084,7 @@ MOE_API moe_status moe_expert_gemm(const void *a, const void *W, int dtype, int 
     if (st != MOE_OK || T == 0) return st;
     if (!a || !W || !offsets || !out || !aligned16(a) || !aligned16(W) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), nullptr, nullptr, out, sorted_tok ? T : T * k,
-                    T * k, E, N, K, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, 0, dev_status};
+                    T * k, E, N, K, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, dev_status};
     return run_gemm(kForward, p, W, N, K, as_cuda(stream));
 }
 
@@ -1015,7 +1095,7 @@ MOE_API moe_status moe_expert_gemm_dgrad(const void *dy, const void *W, int dtyp
     if (st != MOE_OK || T == 0) return st;
     if (!dy || !W || !offsets || !da || !aligned16(dy) || !aligned16(W) || !aligned16(da)) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, nullptr, static_cast<const uint16_t *>(dy), nullptr, nullptr, da,
-                    T * k, T * k, E, K, N, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, 0, dev_status};
+                    T * k, T * k, E, K, N, 0, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0, dev_status};
     return run_gemm(kDgrad, p, W, N, K, as_cuda(stream));
 }
 
@@ -1028,6 +1108,6 @@ MOE_API moe_status moe_expert_gemm_wgrad(const void *dy, const void *a, int dtyp
     if (T > 0 && (!dy || !a || !aligned16(dy) || !aligned16(a))) return MOE_ERR_INVALID_ARG;
     GemmParams p = {offsets, sorted_tok, static_cast<const uint16_t *>(a), static_cast<const uint16_t *>(dy), base, dW,
                     sorted_tok ? T : T * k, T * k, E, K, 0, N, dtype == MOE_BF16, out_dtype == MOE_FP32, 0, 0, 0,
-                    0, dev_status};
+                    dev_status};
     return run_gemm(kWgrad, p, nullptr, N, K, as_cuda(stream));
 }

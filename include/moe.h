@@ -577,8 +577,10 @@ moe_status moe_expert_linear_q4(const moe_q4weights *W, const int32_t *slot_of, 
  *                whose range is not sets MOE_DEV_BAD_INDEX and has no rows
  * Rows that belong to no expert are left as they were; dW is written for every
  * expert, also those without rows (T = 0 among them). Sums run in the tensor
- * cores' fp32, rounded once; their order depends on the sizes only. An fp32
- * result of K = 2048 terms is about 1e-6 off (relative, by norms). N and K are
+ * cores' fp32, rounded once; their order depends on the sizes only. fp32 results
+ * are about 1e-6 off at most (relative, by norms), however long the sum: the
+ * tensor cores cut, so chains of 1024 products are joined by additions that
+ * round; 16-bit results come from chains of 16384. N and K are
  * multiples of 8 up to 16384, E <= 4096; all tensors but offsets and sorted_tok
  * 16-byte aligned; outputs overlap no input (but base).
  */
