@@ -41,6 +41,7 @@ class QMatrix(C.Structure):
 class Q4Weights(C.Structure):
     _fields_ = [("codes", _P), ("scale", _P), ("min", _P), ("num_slots", _I32), ("N", _I32), ("K", _I32),
                 ("group", _I32)]
+    tensors = ()    # kept alive; empty where the addresses were filled in by hand
 
 
 class Swap(C.Structure):
@@ -440,7 +441,7 @@ def q4_weights(codes, scale, min, group: int) -> Q4Weights:
 
 def linear_q4(W: Q4Weights, slot: int, x, T: int, out, act: int = ACT_NONE, stream=None) -> None:
     """out[t] = W[slot] x[t]; out [T][N] (SwiGLU: [T][N/2]) in x's type or fp32."""
-    dev = _place_of(W.tensors[0])
+    dev = _place_of(W.tensors[0] if W.tensors else x)
     code = lib.moe_linear_q4(C.addressof(W), slot, _address(x, T * W.K, dev), dtype_code(x), T, act,
                              _address(out, T * W.N // (1 + (act == ACT_SWIGLU)), dev), dtype_code(out),
                              _stream_on(stream, dev))
@@ -452,7 +453,7 @@ def expert_linear_q4(W: Q4Weights, slot_of, x, T: int, E: int, k: int, offsets, 
                      act: int = ACT_NONE, dev_status=None, stream=None) -> None:
     """out[s] = W[slot_of[e]] x_s for the sorted pairs s of every active expert e
     (x_s = x[sorted_tok[s]], or x[s] with sorted_tok None)."""
-    dev, P = _place_of(W.tensors[0]), T * k
+    dev, P = _place_of(W.tensors[0] if W.tensors else x), T * k
     code = lib.moe_expert_linear_q4(C.addressof(W), _table(slot_of, E, dev),
                                     _address(x, (P if sorted_tok is None else T) * W.K, dev), dtype_code(x), T, E, k,
                                     _table(offsets, E + 1, dev), _table(sorted_tok, P, dev),
