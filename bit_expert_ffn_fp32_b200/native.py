@@ -139,9 +139,9 @@ def stream_handle(stream=None) -> int | None:
     """cudaStream_t of a torch stream, by default the current GPU's current one."""
     if stream is not None:
         return stream.cuda_stream or None
-    import torch
-    # the handle alone: torch.cuda.current_stream() builds a Stream around it (3.4 us a call against 0.3)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+    if _Types.device is None:
+        _Types.load()
+    return _Types.raw_stream(_Types.device()) or None
 
 
 def qmatrix(codes, scale, mn=None, hi=None) -> QMatrix:
@@ -369,7 +369,10 @@ class _Types:
         cls.code = {torch.bfloat16: BF16, torch.int16: BF16, torch.float16: FP16, torch.float32: FP32}
         cls.int32 = torch.int32
         cls.device = torch.cuda.current_device
-        cls.raw_stream = torch._C._cuda_getCurrentRawStream
+        # the handle alone, where torch has it: torch.cuda.current_stream() builds a Stream around it (3.4 us a call
+        # against 0.3)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        cls.raw_stream = staticmethod(raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
 def dtype_code(t) -> int:
