@@ -365,14 +365,15 @@ class _Types:
     @classmethod
     def load(cls) -> None:
         import torch
-        # int16 tensors hold bf16 bits, as for the layer's x
-        cls.code = {torch.bfloat16: BF16, torch.int16: BF16, torch.float16: FP16, torch.float32: FP32}
-        cls.int32 = torch.int32
-        cls.device = torch.cuda.current_device
         # the handle alone, where torch has it: torch.cuda.current_stream() builds a Stream around it (3.4 us a call
         # against 0.3)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         cls.raw_stream = staticmethod(raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        cls.int32 = torch.int32
+        # last, what callers look at to see whether the rest is there: another thread may look meanwhile; int16
+        # tensors hold bf16 bits, as for the layer's x
+        cls.device = torch.cuda.current_device
+        cls.code = {torch.bfloat16: BF16, torch.int16: BF16, torch.float16: FP16, torch.float32: FP32}
 
 
 def dtype_code(t) -> int:
