@@ -471,7 +471,8 @@ def expert_linear_q4(W: Q4Weights, slot_of, x, T: int, E: int, k: int, offsets, 
 def expert_gemm(a, W, T: int, E: int, k: int, N: int, K: int, offsets, sorted_tok, out, dev_status=None,
                 stream=None) -> None:
     """out[s] = W[e] a_s for the sorted pairs s of every expert e
-    (a_s = a[sorted_tok[s]], or a[s] with sorted_tok None)."""
+    (a_s = a[sorted_tok[s]], or a[s] with sorted_tok None). Only dev_status
+    (int32 [1]) tells of a wait that gave up, here and in the two gradients."""
     dev, P, dt = _place_of(W), T * k, dtype_code(a)
     if dtype_code(W) != dt:
         raise ValueError("a and W have one type")

@@ -520,16 +520,18 @@ typedef struct moe_q4weights {
 
 /*
  * out[t] = W[slot] x[t] for T rows x (a projection next to the layer).
- *   x    bf16 or fp16 [T][K] (dtype), 16-byte aligned
+ *   x    bf16 or fp16 [T][K] (dtype)
  *   out  [T][N], with MOE_ACT_SWIGLU [T][N/2], in out_dtype: x's type or MOE_FP32
+ * x and out are 16-byte aligned and do not overlap.
  * Codes (without min: q - 8) enter the products exactly and scales apply to sums
  * of a group in fp32, so no weight is rounded; with min, s*q and m meet only as
  * sums of a group, and where they cancel (a far larger x at a weight near zero),
- * what is left has fp32's digits of either. x enters as fp16, each 128 k of a row scaled by a
- * power of two: values down to 2^-25 of the largest of the 128 are exact, smaller
- * ones are rounded at 2^-36 of it (at 2^-120, where the largest is below 2^-86).
- * An infinity or a NaN in a row of x makes all of that row's results non-finite. The order of the additions depends on the
- * sizes only: equal calls give equal bits.
+ * what is left has fp32's digits of either. x enters as fp16, each 128 k of a row
+ * scaled by a power of two: values down to 2^-25 of the largest of the 128 are
+ * exact, smaller ones are rounded at 2^-36 of it (at 2^-120, where the largest is
+ * below 2^-86). An infinity or a NaN in a row of x makes all of that row's
+ * results non-finite. The order of the additions depends on the sizes only:
+ * equal calls give equal bits.
  * Made for few rows a matrix (decoding, verify batches, small prompts): with
  * more than 8, 16 or 32 of them the codes are read once for each so many rows.
  */
@@ -583,6 +585,10 @@ moe_status moe_expert_linear_q4(const moe_q4weights *W, const int32_t *slot_of, 
  * round; 16-bit results come from chains of 16384. N and K are
  * multiples of 8 up to 16384, E <= 4096; all tensors but offsets and sorted_tok
  * 16-byte aligned; outputs overlap no input (but base).
+ * Every wait inside the kernel is bounded (200 ms for one stage of a tile): one
+ * that runs out sets MOE_DEV_TIMEOUT and drops the tiles that are left, whose
+ * part of the output stays as it was. Only dev_status tells, so pass it and look
+ * at it; with NULL nothing does.
  */
 moe_status moe_expert_gemm(const void *a, const void *W, int dtype, int T, int E, int k, int N, int K,
                            const int32_t *offsets, const int32_t *sorted_tok, void *out, int out_dtype,
