@@ -17,9 +17,10 @@
 // and 8 x apart would cancel: an outlier on a zero weight would take the digits
 // of every other product. x enters as fp16: 128 k of a token are scaled
 // by a power of two that brings their largest to [2^14, 2^15), and the k of the
-// codes at 2^-20 by another 2^-4. bf16 and fp16 values stay exact down to 2^-25
-// of the largest; below that they are rounded at 2^-36 of it, under the 2^-24
-// of the fp32 sums they join. No weight is rounded; in fp32, by group and then
+// codes at 2^-20 by another 2^-4, to [2^10, 2^11) at most. bf16 and fp16 values
+// stay exact down to 2^-24 of the largest (2^-14 of 2^10); below that they are
+// off by half a subnormal, 2^-25 of 2^10, under the 2^-24 of the fp32 sums they
+// join. No weight is rounded; in fp32, by group and then
 // by 128 k:
 //   sum_k w x = 2^-e * (s * 2^24 * sum (q 2^-24) (x 2^e) + m * sum x 2^e)   with min
 //             = 2^-e * s * 2^9 * sum ((q - 8) 2^-9) (x 2^e)                 without

@@ -527,9 +527,9 @@ typedef struct moe_q4weights {
  * of a group in fp32, so no weight is rounded; with min, s*q and m meet only as
  * sums of a group, and where they cancel (a far larger x at a weight near zero),
  * what is left has fp32's digits of either. x enters as fp16, each 128 k of a row
- * scaled by a power of two: values down to 2^-25 of the largest of the 128 are
- * exact, smaller ones are rounded at 2^-36 of it (at 2^-120, where the largest is
- * below 2^-86). An infinity or a NaN in a row of x makes all of that row's
+ * scaled by a power of two: values down to 2^-24 of the largest of the 128 are
+ * exact, smaller ones are off by at most 2^-35 of it (by 2^-121, where the largest
+ * is below 2^-86). An infinity or a NaN in a row of x makes all of that row's
  * results non-finite. The order of the additions depends on the sizes only:
  * equal calls give equal bits.
  * Made for few rows a matrix (decoding, verify batches, small prompts): with
