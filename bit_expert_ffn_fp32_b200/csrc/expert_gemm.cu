@@ -246,8 +246,9 @@ struct Segments {
 };
 template <typename C>
 __device__ __forceinline__ Segments segments_of(const GemmParams &p, int KS) {
-    const int most = p.out_fp32 ? 16 * C::kAccs : 256;
-    const int least = C::kAccs == 1 && p.out_fp32 && KS > 12 ? 2 : 1, count = max(least, (KS + most - 1) / most);
+    constexpr int kMost = 16 * C::kAccs, kFirst = C::kAccs == 1 ? 12 : kMost;  // stages: of a segment, of a single one
+    if (KS <= (p.out_fp32 ? kFirst : 256)) return {1, KS};  // no division on the way of most tiles
+    const int count = p.out_fp32 ? max(2, (KS + kMost - 1) / kMost) : (KS + 255) / 256;
     return {count, (KS + count - 1) / count};
 }
 // Accumulators of a buffer that a segment of `stages` fills.
