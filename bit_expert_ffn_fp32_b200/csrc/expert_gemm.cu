@@ -23,12 +23,13 @@
 // on; two accumulators, so that the epilogue of one tile runs beside the
 // products of the next. Every wait is bounded and sets MOE_DEV_TIMEOUT.
 //
-// Measured (device time of a call): 81,920 pairs by token, 512 experts, 1536 x
-// 2048: 690 us, 78% of the copy bandwidth on its 3.5 GB; dgrad of 4096 tokens,
-// top-10 of 128 experts, the same weights: 216 us at 1.5 GHz (tensor pipe 67%
-// active, DRAM 61%); wgrad of 2048 x 768 for them: 150 us, where MMA and
-// epilogue take turns (5.6 stages a tile); four tokens through 2048 x 768 in
-// fp32: 26 us, 73% of the copy bandwidth.
+// Measured (device time of a call in a burst; back to back, at the sustained
+// clock): 81,920 pairs by token, 512 experts, 1536 x 2048: 653-704 us, 76 to 82%
+// of the copy bandwidth on its 3.5 GB (830 us); dgrad of 4096 tokens, top-10 of
+// 128 experts, the same weights: 228-257 us (298), tensor pipe 69% active, DRAM
+// 60%; wgrad of 2048 x 768 for them: 150 us (181), where MMA and epilogue take
+// turns (5.6 stages a tile); four tokens through 2048 x 768 in fp32: 25-27 us,
+// 69 to 74% of the copy bandwidth.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -577,7 +577,8 @@ moe_status run_q4(const moe_q4weights *W, Q4Params &p, const void *x, int dtype,
     // SM; one, where staging the x of several tokens weighs more than the codes),
     // up to 8 (4 with four token tiles, whose x would not fit); then 16 rows a
     // warp. Where the blocks take several turns anyway, pairs of warps, unless k
-    // is too short to split. Measured (warps a row: us): gate and up rows of one
+    // is too short to split. Measured (warps a row: us; those without min before
+    // q - 8 was formed, which adds 4 to 6%): gate and up rows of one
     // token 1: 13.0, 2: 8.8, 4: 8.2, 8: 10.7 (480 blocks); 8192 x 8192, one token
     // 1: 32, 2: 19, 4: 12.8, 8: 12.1 (256 blocks), five tokens 4: 22, 8: 28; gate
     // and up rows of 37 tokens 1: 91, 2: 79, 4: 89; down rows (3 steps of k) of
